@@ -320,13 +320,128 @@ tq_status tq_search_topk(const tq_quantizer *q, const tq_cache_view *db, int64_t
 typedef enum { TQ_FEED_REGISTERS = 0, TQ_FEED_BULK_STAGED = 1 } tq_decode_feed;
 int32_t tq_set_decode_feed(int32_t feed);
 
+/* ---- paged 4-bit cache: plan, append, read-back, attention -------------
+ *
+ * A serving loop keeps the caches of many sequences in pages of one pool.  A
+ * paged cache is a tq_cache_view whose "batch" is the page and whose "token"
+ * is the place in the page: record (page, h, off) is at
+ *   page*stride_b + h*stride_h + off*stride_n   (in records),
+ * off < page_size.  The SLOT of a token is page*page_size + off, a 64-bit number; -1 means no slot.
+ * A block table [R][table_stride] of int32 holds the pages of each request's
+ * tokens in order, max_pages entries a row of which are used.
+ * The quantizers of these calls are TurboQuant_mse at 4 bits with the
+ * Hadamard rotation; others return TQ_EUNSUPPORTED.
+ *
+ * Lengths, tables, slots and positions are DEVICE arrays that the host does
+ * not see.  A slot or page outside the cache, or a request longer than its
+ * table row, is never followed: the row is skipped (append), read as zeros
+ * (read-back) or left out of the attention, and the next tq_check returns
+ * TQ_EINVAL. */
+
+/* Page plan of one step, from the requests' lengths.  Request r has lens[r]
+ * cached tokens and adds new_lens[r] (negative counts as 0); its new tokens
+ * are rows cu_new[r] .. cu_new[r+1]-1 of the step's token rows.  With
+ * pages(l) = ceil(l / page_size) it needs pages(lens+new) - pages(lens) new
+ * pages, which come off the END of free_pages[0 .. n_free): the requests take
+ * theirs in order.  Writes
+ *   slots[max_tokens]     slot of every token row; -1 behind the last token
+ *                         and for the rows of a request that was refused;
+ *   positions[max_tokens] lens[r] + its place among the new tokens (0 behind);
+ *   cu_new[R + 1]         prefix sums of new_lens;
+ *   seq_lens[R]           lens + new_lens, or lens where refused;
+ *   status[R]             0; 1 refused: free pages run out; 2 refused: more
+ *                         pages than max_pages or rows than max_tokens;
+ *   n_free_out[1]         free pages left;
+ *   block_table           the entries of the new pages, nothing else.
+ * Once a request is refused for pages, so is every later one that needs any;
+ * one that needs none is never refused for pages.  free_pages has free_cap
+ * entries; *n_free (DEVICE) is clamped to 0..free_cap.  Outputs must not
+ * alias inputs (block_table is both: its old pages are read).  R >= 0,
+ * page_size >= 1, max_pages * page_size < 2^31, max_tokens < 2^31. */
+tq_status tq_page_plan(int32_t R, int32_t page_size, const int32_t *lens, const int32_t *new_lens,
+                       const int32_t *free_pages, int64_t free_cap, const int32_t *n_free,
+                       int32_t *block_table, int64_t table_stride, int32_t max_pages,
+                       int64_t max_tokens, int64_t *slots, int32_t *positions, int32_t *cu_new,
+                       int32_t *seq_lens, int32_t *status, int32_t *n_free_out, tq_stream_t stream);
+
+/* Rotary positions on up to 8 axes (time, height, width, ...).  Frequency f
+ * (f < rot_dim / 2) turns by theta = positions[axis[f]][token] * inv_freq[f]:
+ *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin)
+ * on the pair (f, f + rot_dim/2) (TQ_ROPE_HALF) or (2f, 2f+1)
+ * (TQ_ROPE_ADJACENT); coordinates from rot_dim on are left.  rot_dim is a
+ * multiple of 16, at most d.  inv_freq: fp32, axis: int32 or NULL (all axis
+ * 0), both DEVICE, rot_dim / 2 entries.  The angle is the exact product, kept
+ * in double until its whole turns are off, so far positions keep their phase. */
+typedef enum { TQ_ROPE_HALF = 0, TQ_ROPE_ADJACENT = 1 } tq_rope_pairing;
+typedef struct {
+  int32_t rot_dim;
+  int32_t pairing;  /* tq_rope_pairing */
+  int32_t n_axes;   /* 1..8 */
+  const float *inv_freq;
+  const int32_t *axis;
+} tq_rope;
+
+/* Append T token rows to a paged cache: k and v ([T][Hkv][d], dtype) are
+ * encoded into the records at slots[t] of kcache and vcache (rows with slot
+ * -1 are skipped).  With a rope, K is turned before it is encoded (in fp32,
+ * not rounded in between) and the query rows q ([T][Hq][d], the same dtype)
+ * are turned into q_out ([T][Hq][d] contiguous, rounded to dtype; every row,
+ * also those without a slot).  rope NULL: records bit-identical to tq_encode;
+ * then q must be NULL; q may be NULL (Hq = 0) with a rope too.
+ * positions: int32 [n_axes][pos_stride], DEVICE.  Element strides over token
+ * and head; bases and strides times the element size 16-byte aligned, d
+ * contiguous.  Slots must be distinct: where two rows name one slot, its
+ * record is unspecified.  q_out may not overlap an input. */
+tq_status tq_paged_append(const tq_quantizer *kq, const tq_quantizer *vq, const tq_rope *rope,
+                          const int32_t *positions, int64_t pos_stride, tq_dtype dtype, int64_t T,
+                          int32_t Hq, int32_t Hkv, const void *q, int64_t q_stride_t,
+                          int64_t q_stride_h, const void *k, int64_t k_stride_t, int64_t k_stride_h,
+                          const void *v, int64_t v_stride_t, int64_t v_stride_h, void *q_out,
+                          const tq_cache_view *kcache, const tq_cache_view *vcache, int64_t n_pages,
+                          int32_t page_size, const int64_t *slots, tq_stream_t stream);
+
+/* x_hat = ||x|| Pi^T c[idx] of the records at slots[t], every head, into
+ * out[T][H][d] (contiguous, out_dtype): a shared prefix for a dense consumer,
+ * a moved or checked cache.  Rows with slot -1 become zeros. */
+tq_status tq_paged_dequant(const tq_quantizer *q, const tq_cache_view *cache, int64_t n_pages,
+                           int32_t page_size, int64_t T, int32_t H, const int64_t *slots,
+                           tq_dtype out_dtype, void *out, tq_stream_t stream);
+
+/* Attention of ragged query rows over a paged cache.  q: [T][Hq][d] (bf16 or
+ * fp16, DEVICE; element strides over token and head, 16-byte aligned).
+ * Request r owns rows cu_q[r] .. cu_q[r+1]-1 (int32 [R+1], DEVICE, ascending
+ * from 0; NULL: T == R, one row each) and kv_lens[r] cached tokens, those of
+ * its own rows included: row i of n stands at position p = kv_lens[r] - n + i.
+ * causal: it sees tokens j <= p, else all of them; window > 0 (causal only):
+ * and j > p - window.  Query head hq reads kv head hq / (Hq / Hkv).  Logits
+ * are softmax_scale * <q, k_hat>; out: [T][Hq][d] contiguous, q's dtype; lse:
+ * optional [T][Hq] fp32, the natural logarithm of the softmax's sum.  A row
+ * that sees no token gets zeros (lse -inf); rows behind cu_q[R] are left as
+ * they were.  max_q: an upper bound of the requests' row counts; it sizes the
+ * work and never changes which rows are computed.
+ * d is 64, 128 or 256, page_size a multiple of 16, R < 2^24.
+ * workspace: DEVICE, at least tq_paged_attention_workspace_bytes(...) bytes,
+ * 16-byte aligned, else TQ_EWORKSPACE; calls that may overlap on the GPU need
+ * one each. */
+size_t tq_paged_attention_workspace_bytes(int32_t R, int64_t T, int32_t Hq, int32_t Hkv, int32_t d);
+tq_status tq_paged_attention(const tq_quantizer *kq, const tq_quantizer *vq, const void *q,
+                             tq_dtype dtype, int64_t T, int32_t Hq, int32_t Hkv, int64_t q_stride_t,
+                             int64_t q_stride_h, const tq_cache_view *k, const tq_cache_view *v,
+                             int64_t n_pages, int32_t page_size, const int32_t *block_table,
+                             int64_t table_stride, int32_t R, int32_t max_pages,
+                             const int32_t *kv_lens, const int32_t *cu_q, int32_t max_q,
+                             float softmax_scale, int32_t causal, int32_t window, void *out,
+                             float *lse, void *workspace, size_t workspace_bytes, tq_stream_t stream);
+
 /* Synchronize `stream` and report any asynchronous CUDA error, then read and
  * clear the current GPU's fault word, which the kernels set themselves
  * instead of trapping: TQ_ETIMEOUT when a kernel gave up a bounded wait on
  * data that never arrived (about a second; the outputs of that call are not
  * valid), TQ_ECUDA when a decode launch found its shared-memory layout
- * invalid and wrote nothing.  The word is per GPU, not per stream: it
- * reports every such fault on the device since the last tq_check. */
+ * invalid and wrote nothing, TQ_EINVAL when a paged call met a slot, page or
+ * length outside its cache (that access was skipped).  The word is per GPU,
+ * not per stream: it reports every such fault on the device since the last
+ * tq_check. */
 tq_status tq_check(tq_stream_t stream);
 
 const char *tq_status_string(tq_status s);

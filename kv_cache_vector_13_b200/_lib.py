@@ -16,6 +16,7 @@ TQ_MSE, TQ_PROD = 0, 1
 TQ_ROT_HADAMARD, TQ_ROT_DENSE = 0, 1
 TQ_CB_GAUSS, TQ_CB_BETA = 0, 1
 TQ_F32, TQ_BF16, TQ_F16 = 0, 1, 2
+TQ_ROPE_HALF, TQ_ROPE_ADJACENT = 0, 1  # tq_rope_pairing
 TQ_NOALLOC_SCRATCH_BYTES = 16 << 20  # include/tq.h
 
 # every symbol include/tq.h declares
@@ -25,6 +26,8 @@ EXPORTS = (
     "tq_append_decode_attention", "tq_decode_attention_noalloc",
     "tq_search_workspace_bytes", "tq_search_topk",
     "tq_decode_split_workspace_bytes", "tq_decode_attention_split",
+    "tq_page_plan", "tq_paged_append", "tq_paged_dequant",
+    "tq_paged_attention_workspace_bytes", "tq_paged_attention",
     "tq_set_decode_feed", "tq_check", "tq_status_string", "tq_last_error", "tq_version",
 )
 
@@ -41,6 +44,12 @@ class TqCacheView(ctypes.Structure):
     _fields_ = [
         ("codes", c_void_p), ("qjl", c_void_p), ("norms", c_void_p), ("rnorms", c_void_p),
         ("stride_b", c_int64), ("stride_h", c_int64), ("stride_n", c_int64),
+    ]
+
+
+class TqRope(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", c_int32), ("pairing", c_int32), ("n_axes", c_int32), ("inv_freq", c_void_p), ("axis", c_void_p),
     ]
 
 
@@ -109,6 +118,24 @@ def lib() -> ctypes.CDLL:
         POINTER(TqQuantizer), POINTER(TqQuantizer), c_void_p, c_int32, c_int32, c_int32, c_int32, c_int64,
         c_void_p, POINTER(TqCacheView), POINTER(TqCacheView), c_float, c_void_p, c_void_p, c_size_t, c_void_p]
     L.tq_decode_attention_split.restype = c_int32
+    L.tq_page_plan.argtypes = [c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int64,
+                               c_int32, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]
+    L.tq_page_plan.restype = c_int32
+    L.tq_paged_append.argtypes = [
+        POINTER(TqQuantizer), POINTER(TqQuantizer), POINTER(TqRope), c_void_p, c_int64, c_int32, c_int64, c_int32,
+        c_int32, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_void_p,
+        POINTER(TqCacheView), POINTER(TqCacheView), c_int64, c_int32, c_void_p, c_void_p]
+    L.tq_paged_append.restype = c_int32
+    L.tq_paged_dequant.argtypes = [POINTER(TqQuantizer), POINTER(TqCacheView), c_int64, c_int32, c_int64, c_int32,
+                                   c_void_p, c_int32, c_void_p, c_void_p]
+    L.tq_paged_dequant.restype = c_int32
+    L.tq_paged_attention_workspace_bytes.argtypes = [c_int32, c_int64, c_int32, c_int32, c_int32]
+    L.tq_paged_attention_workspace_bytes.restype = c_size_t
+    L.tq_paged_attention.argtypes = [
+        POINTER(TqQuantizer), POINTER(TqQuantizer), c_void_p, c_int32, c_int64, c_int32, c_int32, c_int64, c_int64,
+        POINTER(TqCacheView), POINTER(TqCacheView), c_int64, c_int32, c_void_p, c_int64, c_int32, c_int32, c_void_p,
+        c_void_p, c_int32, c_float, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]
+    L.tq_paged_attention.restype = c_int32
     L.tq_set_decode_feed.argtypes = [c_int32]
     L.tq_set_decode_feed.restype = c_int32
     L.tq_check.argtypes = [c_void_p]

@@ -350,6 +350,225 @@ def search_topk(qz: Quantizer, queries: torch.Tensor, db: PackedCache, k: int):
     return Search(qz, queries.shape[0], n_db, device=queries.device)(queries, db, k)
 
 
+# ------------------------------------------------------------ paged cache
+
+def _on(t: torch.Tensor, stream=None):
+    """(device guard, stream handle) of a call whose tensors live with t."""
+    s = stream if stream is not None else torch.cuda.current_stream(t.device)
+    return torch.cuda.device(t.device), s.cuda_stream
+
+
+def _strides(t: Optional[torch.Tensor]):
+    """Element strides over the first two dims (0 where the extent is 1)."""
+    return (0, 0) if t is None else tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1))
+
+
+def _same_device(t: torch.Tensor, **others) -> None:
+    for name, o in others.items():
+        assert o is None or o.device == t.device, f"{name} is on {o.device}, not on {t.device}"
+
+
+def _check_i32(**ts) -> None:
+    for name, t in ts.items():
+        assert t is None or (t.dtype == torch.int32 and t.is_contiguous()), f"{name}: a contiguous int32 tensor"
+
+
+@dataclass
+class PagePlan:
+    """Outputs of tq_page_plan (views of the planner's buffers, overwritten
+    by its next call)."""
+    slots: torch.Tensor      # [max_tokens] int64, -1 where there is none
+    positions: torch.Tensor  # [max_tokens] int32
+    cu_new: torch.Tensor     # [R + 1] int32
+    seq_lens: torch.Tensor   # [R] int32, new tokens included
+    status: torch.Tensor     # [R] int32: 0, or why a request was refused
+    n_free: torch.Tensor     # [1] int32, free pages left
+
+
+class PagePlanner:
+    """Reusable tq_page_plan call for n_requests requests and at most
+    max_tokens new token rows (its outputs allocated once)."""
+
+    def __init__(self, n_requests: int, page_size: int, max_tokens: int, device="cuda"):
+        self.R, self.page_size, self.max_tokens = n_requests, page_size, max_tokens
+        i32 = dict(dtype=torch.int32, device=device)
+        self.plan = PagePlan(torch.empty(max_tokens, dtype=torch.int64, device=device), torch.empty(max_tokens, **i32),
+                             torch.empty(n_requests + 1, **i32), torch.empty(n_requests, **i32),
+                             torch.empty(n_requests, **i32), torch.empty(1, **i32))
+
+    def __call__(self, lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, n_free: torch.Tensor,
+                 block_table: torch.Tensor, stream=None) -> PagePlan:
+        """Give the new_lens [R] tokens that requests of lens [R] cached ones
+        add their slots; new pages come off the end of free_pages[:n_free]
+        (n_free: a one-element int32 device tensor) and are entered in
+        block_table [R, max_pages] (int32, in place).  Pass plan.seq_lens and
+        plan.n_free on by copying them: they may not be this call's inputs."""
+        p = self.plan
+        assert lens.shape == (self.R,) and new_lens.shape == (self.R,) and n_free.numel() == 1
+        assert block_table.dim() == 2 and block_table.shape[0] == self.R and free_pages.dim() == 1
+        assert block_table.dtype == torch.int32 and (block_table.shape[1] <= 1 or block_table.stride(1) == 1)
+        _check_i32(lens=lens, new_lens=new_lens, free_pages=free_pages, n_free=n_free)
+        _same_device(p.slots, lens=lens, new_lens=new_lens, free_pages=free_pages, n_free=n_free,
+                     block_table=block_table)
+        guard, s = _on(lens, stream)
+        with guard:
+            L.check(L.lib().tq_page_plan(
+                self.R, self.page_size, _ptr(lens), _ptr(new_lens), _ptr(free_pages), free_pages.numel(), _ptr(n_free),
+                _ptr(block_table), max(block_table.stride(0), 0), block_table.shape[1], self.max_tokens, _ptr(p.slots),
+                _ptr(p.positions), _ptr(p.cu_new), _ptr(p.seq_lens), _ptr(p.status), _ptr(p.n_free), s))
+        return p
+
+
+class Rope:
+    """Rotary positions on several axes (tq_rope): inv_freq [rot_dim / 2]
+    (fp32, on the device), and which axis turns which frequency, either as
+    sections (how many consecutive frequencies each axis has) or as axis
+    [rot_dim / 2] itself; neither means one axis.  pairing "half" turns the
+    coordinates (f, f + rot_dim/2), "adjacent" (2f, 2f + 1)."""
+
+    def __init__(self, inv_freq: torch.Tensor, sections=None, axis=None, pairing: str = "half"):
+        assert pairing in ("half", "adjacent") and inv_freq.dim() == 1
+        assert sections is None or axis is None
+        self.inv_freq = inv_freq.to(torch.float32).contiguous()
+        n = self.inv_freq.numel()
+        if sections is not None:
+            assert sum(sections) == n and all(c >= 0 for c in sections), "sections must cover the frequencies"
+            axis = [a for a, c in enumerate(sections) for _ in range(c)]
+            self.n_axes = len(sections)
+        elif axis is not None:
+            axis = [int(a) for a in axis]
+            assert len(axis) == n and all(a >= 0 for a in axis)
+            self.n_axes = max(axis) + 1
+        else:
+            self.n_axes = 1
+        self.axis = None if axis is None else torch.tensor(axis, dtype=torch.int32).to(inv_freq.device)
+        self.pairing, self.rot_dim = pairing, 2 * n
+        self._c = L.TqRope(2 * n, L.TQ_ROPE_ADJACENT if pairing == "adjacent" else L.TQ_ROPE_HALF, self.n_axes,
+                           _ptr(self.inv_freq), _ptr(self.axis))
+
+    def c_struct(self) -> L.TqRope:
+        return self._c
+
+
+def paged_append(kq: Quantizer, vq: Quantizer, k: torch.Tensor, v: torch.Tensor, kcache: PackedCache,
+                 vcache: PackedCache, slots: torch.Tensor, q: Optional[torch.Tensor] = None,
+                 rope: Optional[Rope] = None, positions: Optional[torch.Tensor] = None,
+                 q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """tq_paged_append: encode k and v [T, Hkv, d] into the records at
+    slots [T] (int64; -1 skips a row) of kcache and vcache (empty_cache(qz,
+    n_pages, Hkv, page_size)).  With a rope, k and the query rows q [T, Hq, d]
+    are turned to positions ([T] or [n_axes, T], int32) first, and the turned
+    q is returned (q_out, or a new tensor)."""
+    T, Hkv, d = k.shape
+    assert d == kq.d and v.shape == k.shape and v.dtype == k.dtype and k.dtype in _DTYPES
+    assert k.stride(2) == 1 and v.stride(2) == 1
+    assert slots.shape == (T,) and slots.dtype == torch.int64 and slots.is_contiguous()
+    n_pages, H, P = kcache.shape
+    assert H == Hkv and vcache.shape == kcache.shape
+    pos_stride = 0
+    if rope is not None:
+        assert positions is not None and positions.dtype == torch.int32
+        assert positions.shape == (rope.n_axes, T) or (rope.n_axes == 1 and positions.shape == (T,))
+        assert T <= 1 or positions.stride(-1) == 1
+        pos_stride = positions.stride(0) if rope.n_axes > 1 else 0
+    else:
+        assert q is None and positions is None, "query rows and positions need a rope"
+    Hq = 0
+    if q is not None:
+        Hq = q.shape[1]
+        assert q.shape == (T, Hq, d) and q.dtype == k.dtype and q.stride(2) == 1
+        if q_out is None:
+            q_out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+        assert q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.is_contiguous()
+    _same_device(k, v=v, q=q, q_out=q_out, slots=slots, positions=positions, kcache=kcache.norms,
+                 vcache=vcache.norms, kq=kq.centroids, vq=vq.centroids,
+                 rope=None if rope is None else rope.inv_freq)
+    kv, vv = kcache.view(), vcache.view()
+    guard, s = _on(k, stream)
+    with guard:
+        L.check(L.lib().tq_paged_append(
+            ctypes.byref(kq.c_struct()), ctypes.byref(vq.c_struct()),
+            None if rope is None else ctypes.byref(rope.c_struct()), _ptr(positions), pos_stride, _DTYPES[k.dtype], T,
+            Hq, Hkv, _ptr(q), *_strides(q), _ptr(k), *_strides(k), _ptr(v), *_strides(v),
+            _ptr(q_out) if q is not None else None, ctypes.byref(kv), ctypes.byref(vv), n_pages, P, _ptr(slots), s))
+    return q_out if q is not None else None
+
+
+def paged_dequant(qz: Quantizer, cache: PackedCache, slots: torch.Tensor, dtype=torch.float32,
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """tq_paged_dequant: the vectors of the records at slots [T] (int64; -1
+    gives zeros) as [T, H, d] in dtype."""
+    n_pages, H, P = cache.shape
+    assert slots.dim() == 1 and slots.dtype == torch.int64 and slots.is_contiguous()
+    T = slots.shape[0]
+    if out is None:
+        out = torch.empty((T, H, qz.d), dtype=dtype, device=cache.norms.device)
+    assert out.shape == (T, H, qz.d) and out.dtype in _DTYPES and out.is_contiguous()
+    _same_device(out, slots=slots, cache=cache.norms, qz=qz.centroids)
+    v = cache.view()
+    guard, s = _on(out, stream)
+    with guard:
+        L.check(L.lib().tq_paged_dequant(ctypes.byref(qz.c_struct()), ctypes.byref(v), n_pages, P, T, H, _ptr(slots),
+                                         _DTYPES[out.dtype], _ptr(out), s))
+    return out
+
+
+class PagedAttention:
+    """Reusable tq_paged_attention call for batches of at most max_requests
+    requests and max_tokens query rows (its workspace allocated once).  Calls
+    that may overlap on the GPU need an object each."""
+
+    def __init__(self, kq: Quantizer, vq: Quantizer, Hq: int, Hkv: int, max_requests: int, max_tokens: int,
+                 device="cuda"):
+        self.kq, self.vq, self.Hq, self.Hkv = kq, vq, Hq, Hkv
+        self.max_requests, self.max_tokens = max_requests, max_tokens
+        with torch.cuda.device(torch.device(device)):
+            nb = int(L.lib().tq_paged_attention_workspace_bytes(max_requests, max_tokens, Hq, Hkv, kq.d))
+        self.workspace = torch.empty(max(nb, 16), dtype=torch.uint8, device=device)
+        self.ws_bytes = nb
+
+    def __call__(self, q: torch.Tensor, kcache: PackedCache, vcache: PackedCache, block_table: torch.Tensor,
+                 kv_lens: torch.Tensor, cu_q: Optional[torch.Tensor] = None, max_q: Optional[int] = None,
+                 scale: Optional[float] = None, causal: bool = True, window: int = 0,
+                 out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+        """Attention of the query rows q [T, Hq, d] (bf16 or fp16): request r
+        owns rows cu_q[r]:cu_q[r+1] (cu_q None: one row each), its cached
+        tokens are the kv_lens[r] ones of the pages block_table[r] (its own
+        rows' included).  max_q: an upper bound of the row counts (default:
+        1 without cu_q, else T).  Returns out [T, Hq, d] in q's dtype; lse
+        [T, Hq] (fp32), if given, gets the logarithm of the softmax's sums."""
+        T, Hq, d = q.shape
+        R = kv_lens.shape[0]
+        n_pages, Hkv, P = kcache.shape
+        assert (Hq, Hkv, d) == (self.Hq, self.Hkv, self.kq.d) and q.dtype in _DTYPES and q.stride(2) == 1
+        assert vcache.shape == kcache.shape
+        assert R <= self.max_requests and T <= self.max_tokens, "more requests or rows than the workspace is for"
+        assert block_table.dim() == 2 and block_table.shape[0] == R and block_table.dtype == torch.int32
+        assert block_table.shape[1] <= 1 or block_table.stride(1) == 1
+        assert cu_q is None or cu_q.shape == (R + 1,)
+        _check_i32(kv_lens=kv_lens, cu_q=cu_q)
+        if max_q is None:
+            max_q = 1 if cu_q is None else max(T, 1)
+        if scale is None:
+            scale = 1.0 / math.sqrt(d)
+        if out is None:
+            out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+        assert out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()
+        assert lse is None or (lse.shape == (T, Hq) and lse.dtype == torch.float32 and lse.is_contiguous())
+        _same_device(q, kcache=kcache.norms, vcache=vcache.norms, block_table=block_table, kv_lens=kv_lens, cu_q=cu_q,
+                     out=out, lse=lse, workspace=self.workspace, kq=self.kq.centroids, vq=self.vq.centroids)
+        kv, vv = kcache.view(), vcache.view()
+        guard, s = _on(q, stream)
+        with guard:
+            L.check(L.lib().tq_paged_attention(
+                ctypes.byref(self.kq.c_struct()), ctypes.byref(self.vq.c_struct()), _ptr(q), _DTYPES[q.dtype], T, Hq,
+                Hkv, *_strides(q), ctypes.byref(kv), ctypes.byref(vv), n_pages, P, _ptr(block_table),
+                max(block_table.stride(0), 0), R, block_table.shape[1], _ptr(kv_lens), _ptr(cu_q), max_q, float(scale),
+                int(causal), int(window), _ptr(out), _ptr(lse), _ptr(self.workspace), self.ws_bytes, s))
+        return out
+
+
 def set_decode_feed(staged: bool) -> bool:
     """Feed of the tensor-core decode for this process: bulk-copy staging
     through shared memory (True) or straight into registers (False, the

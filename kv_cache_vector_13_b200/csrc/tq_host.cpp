@@ -22,6 +22,7 @@
 
 #include "../../include/tq.h"
 #include "tq_internal.h"
+#include "tq_paged.h"
 
 #include <cuda_runtime.h>
 
@@ -726,6 +727,258 @@ tq_status tq_search_topk(const tq_quantizer *q, const tq_cache_view *db, int64_t
   return TQ_OK;
 }
 
+}  // extern "C"
+
+namespace {
+
+// A quantizer of the paged calls: TurboQuant_mse, 4 bits, Hadamard.
+tq_status check_paged_quantizer(const tq_quantizer *q, const char *name, tq::QuantParams *out) {
+  const tq_status st = check_quantizer(q, name, out);
+  if (st != TQ_OK) return st;
+  if (out->prod || out->bm != 4 || out->rot)
+    return fail(TQ_EUNSUPPORTED, "%s: the paged cache takes TurboQuant_mse at 4 bits with the Hadamard rotation", name);
+  return TQ_OK;
+}
+
+tq_status check_pages(const char *name, int64_t n_pages, int32_t page_size) {
+  if (n_pages < 0 || n_pages > INT32_MAX) return fail(TQ_EINVAL, "%s: n_pages=%lld", name, (long long)n_pages);
+  if (page_size < 1) return fail(TQ_EINVAL, "%s: page_size=%d", name, page_size);
+  return TQ_OK;
+}
+
+bool valid_dtype(int dt) { return dt == TQ_F32 || dt == TQ_BF16 || dt == TQ_F16; }
+
+// Rows [T][H][d] by (token, head) element strides, 16-byte aligned.
+tq_status check_rows(const char *name, const char *what, const void *p, size_t es, int64_t st, int64_t sh) {
+  if (!p || !aligned(p, 16)) return fail(TQ_EINVAL, "%s: %s NULL or not 16-byte aligned", name, what);
+  if (st < 0 || sh < 0 || (st * es) % 16 || (sh * es) % 16)
+    return fail(TQ_EINVAL, "%s: the strides of %s must be 16-byte aligned and not negative", name, what);
+  return TQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+tq_status tq_page_plan(int32_t R, int32_t page_size, const int32_t *lens, const int32_t *new_lens,
+                       const int32_t *free_pages, int64_t free_cap, const int32_t *n_free, int32_t *block_table,
+                       int64_t table_stride, int32_t max_pages, int64_t max_tokens, int64_t *slots,
+                       int32_t *positions, int32_t *cu_new, int32_t *seq_lens, int32_t *status,
+                       int32_t *n_free_out, tq_stream_t stream) {
+  const char *name = "tq_page_plan";
+  if (R < 0 || max_pages < 0 || max_tokens < 0 || free_cap < 0 || table_stride < 0)
+    return fail(TQ_EINVAL, "%s: negative size", name);
+  if (page_size < 1) return fail(TQ_EINVAL, "%s: page_size=%d", name, page_size);
+  if ((int64_t)max_pages * page_size > INT32_MAX || max_tokens > INT32_MAX || free_cap > INT32_MAX)
+    return fail(TQ_EINVAL, "%s: max_pages * page_size, max_tokens and free_cap must be below 2^31", name);
+  if (R > 1 && table_stride < max_pages)
+    return fail(TQ_EINVAL, "%s: table_stride=%lld is below max_pages=%d", name, (long long)table_stride, max_pages);
+  if (!n_free || !cu_new || !n_free_out || !aligned(n_free, 4) || !aligned(cu_new, 4) || !aligned(n_free_out, 4))
+    return fail(TQ_EINVAL, "%s: n_free, cu_new or n_free_out NULL or misaligned", name);
+  if (R > 0 && (!lens || !new_lens || !seq_lens || !status || !aligned(lens, 4) || !aligned(new_lens, 4) ||
+                !aligned(seq_lens, 4) || !aligned(status, 4)))
+    return fail(TQ_EINVAL, "%s: a per-request array is NULL or misaligned", name);
+  if (R > 0 && max_pages > 0 && (!block_table || !aligned(block_table, 4)))
+    return fail(TQ_EINVAL, "%s: block_table NULL or misaligned", name);
+  if (free_cap > 0 && (!free_pages || !aligned(free_pages, 4)))
+    return fail(TQ_EINVAL, "%s: free_pages NULL or misaligned", name);
+  if (max_tokens > 0 && (!slots || !positions || !aligned(slots, 8) || !aligned(positions, 4)))
+    return fail(TQ_EINVAL, "%s: slots or positions NULL or misaligned", name);
+  if (n_free == n_free_out || (R > 0 && (lens == seq_lens || new_lens == seq_lens)))
+    return fail(TQ_EINVAL, "%s: an output aliases an input", name);
+  tq::PagePlanArgs a{R, page_size, max_pages, lens, new_lens, free_pages, n_free, free_cap, block_table,
+                     table_stride, max_tokens, slots, positions, cu_new, seq_lens, status, n_free_out};
+  const cudaError_t e = tq::launch_page_plan(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? TQ_OK : cuda_fail(e, "tq_page_plan launch");
+}
+
+tq_status tq_paged_append(const tq_quantizer *kq, const tq_quantizer *vq, const tq_rope *rope,
+                          const int32_t *positions, int64_t pos_stride, tq_dtype dtype, int64_t T, int32_t Hq,
+                          int32_t Hkv, const void *q, int64_t q_stride_t, int64_t q_stride_h, const void *k,
+                          int64_t k_stride_t, int64_t k_stride_h, const void *v, int64_t v_stride_t,
+                          int64_t v_stride_h, void *q_out, const tq_cache_view *kcache, const tq_cache_view *vcache,
+                          int64_t n_pages, int32_t page_size, const int64_t *slots, tq_stream_t stream) {
+  const char *name = "tq_paged_append";
+  tq::PagedAppendArgs a{};
+  tq_status st = check_paged_quantizer(kq, "tq_paged_append(kq)", &a.kq);
+  if (st != TQ_OK) return st;
+  st = check_paged_quantizer(vq, "tq_paged_append(vq)", &a.vq);
+  if (st != TQ_OK) return st;
+  if (a.kq.d != a.vq.d) return fail(TQ_EINVAL, "%s: K d=%d but V d=%d", name, a.kq.d, a.vq.d);
+  if (!valid_dtype(dtype)) return fail(TQ_EINVAL, "%s: dtype=%d", name, (int)dtype);
+  st = check_pages(name, n_pages, page_size);
+  if (st != TQ_OK) return st;
+  if (T < 0 || T > INT32_MAX || Hq < 0 || Hkv < 0) return fail(TQ_EINVAL, "%s: a size is out of range", name);
+  if (Hq > 65536 || Hkv > 65536) return fail(TQ_EINVAL, "%s: more than 65536 heads", name);
+  if (!q) Hq = 0;
+  if (rope) {
+    if (rope->rot_dim < 16 || rope->rot_dim > a.kq.d || rope->rot_dim % 16)
+      return fail(TQ_EINVAL, "%s: rot_dim=%d (expected a multiple of 16 up to d=%d)", name, rope->rot_dim, a.kq.d);
+    if (rope->pairing != TQ_ROPE_HALF && rope->pairing != TQ_ROPE_ADJACENT)
+      return fail(TQ_EINVAL, "%s: pairing=%d", name, rope->pairing);
+    if (rope->n_axes < 1 || rope->n_axes > 8) return fail(TQ_EINVAL, "%s: n_axes=%d (expected 1..8)", name, rope->n_axes);
+    if (!rope->inv_freq || !aligned(rope->inv_freq, 4) || (rope->axis && !aligned(rope->axis, 4)))
+      return fail(TQ_EINVAL, "%s: inv_freq NULL, or it or axis misaligned", name);
+    if (rope->n_axes > 1 && !rope->axis) return fail(TQ_EINVAL, "%s: several axes without an axis list", name);
+    if (T > 0 && (!positions || !aligned(positions, 4))) return fail(TQ_EINVAL, "%s: positions NULL or misaligned", name);
+    if (rope->n_axes > 1 && pos_stride < T)
+      return fail(TQ_EINVAL, "%s: pos_stride=%lld is below T=%lld", name, (long long)pos_stride, (long long)T);
+  } else if (Hq > 0) {
+    return fail(TQ_EINVAL, "%s: query rows without a rope", name);
+  }
+  if (T == 0 || (Hkv == 0 && Hq == 0)) return TQ_OK;
+  const size_t es = dtype_size(dtype);
+  if (Hq > 0) {
+    st = check_rows(name, "q", q, es, q_stride_t, q_stride_h);
+    if (st != TQ_OK) return st;
+    if (!q_out || !aligned(q_out, 16) || q_out == q) return fail(TQ_EINVAL, "%s: q_out NULL, not 16-byte aligned, or q itself", name);
+  }
+  if (Hkv > 0) {
+    st = check_rows(name, "k", k, es, k_stride_t, k_stride_h);
+    if (st != TQ_OK) return st;
+    st = check_rows(name, "v", v, es, v_stride_t, v_stride_h);
+    if (st != TQ_OK) return st;
+  }
+  st = check_view(kcache, a.kq, "tq_paged_append(kcache)", n_pages > 0 && Hkv > 0, &a.kc);
+  if (st != TQ_OK) return st;
+  st = check_view(vcache, a.vq, "tq_paged_append(vcache)", n_pages > 0 && Hkv > 0, &a.vc);
+  if (st != TQ_OK) return st;
+  if (!slots || !aligned(slots, 8)) return fail(TQ_EINVAL, "%s: slots NULL or misaligned", name);
+  a.dtype = dtype;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_st = q_stride_t;
+  a.q_sh = q_stride_h;
+  a.k_st = k_stride_t;
+  a.k_sh = k_stride_h;
+  a.v_st = v_stride_t;
+  a.v_sh = v_stride_h;
+  a.q_out = q_out;
+  a.n_slots = n_pages * page_size;
+  a.page_size = page_size;
+  a.slots = slots;
+  if (rope) {
+    a.rot_dim = rope->rot_dim;
+    a.adjacent = rope->pairing == TQ_ROPE_ADJACENT;
+    a.inv_freq = rope->inv_freq;
+    a.axis = rope->axis;
+    a.n_axes = rope->n_axes;
+    a.positions = positions;
+    a.pos_stride = pos_stride;
+  }
+  const cudaError_t e = tq::launch_paged_append(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? TQ_OK : cuda_fail(e, "tq_paged_append launch");
+}
+
+tq_status tq_paged_dequant(const tq_quantizer *q, const tq_cache_view *cache, int64_t n_pages, int32_t page_size,
+                           int64_t T, int32_t H, const int64_t *slots, tq_dtype out_dtype, void *out,
+                           tq_stream_t stream) {
+  const char *name = "tq_paged_dequant";
+  tq::PagedDequantArgs a{};
+  tq_status st = check_paged_quantizer(q, name, &a.q);
+  if (st != TQ_OK) return st;
+  if (!valid_dtype(out_dtype)) return fail(TQ_EINVAL, "%s: out_dtype=%d", name, (int)out_dtype);
+  st = check_pages(name, n_pages, page_size);
+  if (st != TQ_OK) return st;
+  if (T < 0 || T > INT32_MAX || H < 0) return fail(TQ_EINVAL, "%s: a size is out of range", name);
+  if (T == 0 || H == 0) return TQ_OK;
+  st = check_view(cache, a.q, name, n_pages > 0, &a.c);
+  if (st != TQ_OK) return st;
+  if (!slots || !aligned(slots, 8)) return fail(TQ_EINVAL, "%s: slots NULL or misaligned", name);
+  if (!out || !aligned(out, 16)) return fail(TQ_EINVAL, "%s: out NULL or not 16-byte aligned", name);
+  a.T = T;
+  a.H = H;
+  a.n_slots = n_pages * page_size;
+  a.page_size = page_size;
+  a.slots = slots;
+  a.out_dtype = out_dtype;
+  a.out = out;
+  const cudaError_t e = tq::launch_paged_dequant(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? TQ_OK : cuda_fail(e, "tq_paged_dequant launch");
+}
+
+size_t tq_paged_attention_workspace_bytes(int32_t R, int64_t T, int32_t Hq, int32_t Hkv, int32_t d) {
+  if (R <= 0 || T <= 0 || T > INT32_MAX || Hq <= 0 || Hkv <= 0 || Hq % Hkv || !valid_d(d)) return 0;
+  return tq::paged_attention_workspace(R, T, Hq, Hkv, d);
+}
+
+tq_status tq_paged_attention(const tq_quantizer *kq, const tq_quantizer *vq, const void *q, tq_dtype dtype, int64_t T,
+                             int32_t Hq, int32_t Hkv, int64_t q_stride_t, int64_t q_stride_h, const tq_cache_view *k,
+                             const tq_cache_view *v, int64_t n_pages, int32_t page_size, const int32_t *block_table,
+                             int64_t table_stride, int32_t R, int32_t max_pages, const int32_t *kv_lens,
+                             const int32_t *cu_q, int32_t max_q, float softmax_scale, int32_t causal, int32_t window,
+                             void *out, float *lse, void *workspace, size_t workspace_bytes, tq_stream_t stream) {
+  const char *name = "tq_paged_attention";
+  tq::PagedAttentionArgs a{};
+  tq_status st = check_paged_quantizer(kq, "tq_paged_attention(kq)", &a.kq);
+  if (st != TQ_OK) return st;
+  st = check_paged_quantizer(vq, "tq_paged_attention(vq)", &a.vq);
+  if (st != TQ_OK) return st;
+  if (a.kq.d != a.vq.d) return fail(TQ_EINVAL, "%s: K d=%d but V d=%d", name, a.kq.d, a.vq.d);
+  if (!valid_dtype(dtype)) return fail(TQ_EINVAL, "%s: dtype=%d", name, (int)dtype);
+  if (dtype == TQ_F32) return fail(TQ_EUNSUPPORTED, "%s: fp32 query rows (bf16 and fp16 are built)", name);
+  st = check_pages(name, n_pages, page_size);
+  if (st != TQ_OK) return st;
+  if (page_size % 16) return fail(TQ_EUNSUPPORTED, "%s: page_size=%d is not a multiple of 16", name, page_size);
+  if (T < 0 || T > INT32_MAX || Hq < 0 || R < 0 || max_pages < 0 || table_stride < 0)
+    return fail(TQ_EINVAL, "%s: a size is out of range", name);
+  if (R >= 1 << 24) return fail(TQ_EINVAL, "%s: R=%d is 2^24 or more", name, R);
+  if (Hkv <= 0 || Hq % Hkv) return fail(TQ_EINVAL, "%s: Hq=%d not a multiple of Hkv=%d", name, Hq, Hkv);
+  if (Hq > 65535) return fail(TQ_EINVAL, "%s: more than 65535 heads", name);
+  if ((int64_t)max_pages * page_size > INT32_MAX)
+    return fail(TQ_EINVAL, "%s: max_pages * page_size must be below 2^31", name);
+  if (R > 1 && table_stride < max_pages)
+    return fail(TQ_EINVAL, "%s: table_stride=%lld is below max_pages=%d", name, (long long)table_stride, max_pages);
+  if (!std::isfinite(softmax_scale)) return fail(TQ_EINVAL, "%s: softmax_scale not finite", name);
+  if (window < 0 || (window > 0 && !causal)) return fail(TQ_EINVAL, "%s: window=%d causal=%d", name, window, causal);
+  if (max_q < 1) return fail(TQ_EINVAL, "%s: max_q=%d", name, max_q);
+  if (T == 0 || R == 0 || Hq == 0) return TQ_OK;
+  if (!cu_q && T != R) return fail(TQ_EINVAL, "%s: T=%lld rows for R=%d requests without cu_q", name, (long long)T, R);
+  st = check_rows(name, "q", q, 2, q_stride_t, q_stride_h);
+  if (st != TQ_OK) return st;
+  if (!out || !aligned(out, 16) || out == q) return fail(TQ_EINVAL, "%s: out NULL, not 16-byte aligned, or q itself", name);
+  if (lse && !aligned(lse, 4)) return fail(TQ_EINVAL, "%s: lse misaligned", name);
+  if (!kv_lens || !aligned(kv_lens, 4) || (cu_q && !aligned(cu_q, 4)))
+    return fail(TQ_EINVAL, "%s: kv_lens NULL, or it or cu_q misaligned", name);
+  if (max_pages > 0 && (!block_table || !aligned(block_table, 4)))
+    return fail(TQ_EINVAL, "%s: block_table NULL or misaligned", name);
+  st = check_view(k, a.kq, "tq_paged_attention(k)", n_pages > 0, &a.k);
+  if (st != TQ_OK) return st;
+  st = check_view(v, a.vq, "tq_paged_attention(v)", n_pages > 0, &a.v);
+  if (st != TQ_OK) return st;
+  const size_t need = tq_paged_attention_workspace_bytes(R, T, Hq, Hkv, a.kq.d);
+  if (workspace_bytes < need || !workspace || !aligned(workspace, 16))
+    return fail(TQ_EWORKSPACE, "%s: workspace %zu bytes, need %zu (16-byte aligned)", name, workspace_bytes, need);
+  a.dtype = dtype;
+  a.q = q;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.q_st = q_stride_t;
+  a.q_sh = q_stride_h;
+  a.n_pages = n_pages;
+  a.page_size = page_size;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.R = R;
+  a.max_pages = max_pages;
+  a.kv_lens = kv_lens;
+  a.cu_q = cu_q;
+  a.max_q = max_q;
+  a.scale = softmax_scale;
+  a.causal = causal != 0;
+  a.window = window;
+  a.out = out;
+  a.lse = lse;
+  a.ws = workspace;
+  const cudaError_t e = tq::launch_paged_attention(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? TQ_OK : cuda_fail(e, "tq_paged_attention launch");
+}
+
 tq_status tq_check(tq_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "tq_check");
@@ -739,6 +992,8 @@ tq_status tq_check(tq_stream_t stream) {
                              "its outputs are not valid");
   if (faults & tq::kFaultSmemLayout)
     return fail(TQ_ECUDA, "tq_check: a decode kernel found its shared-memory layout invalid and wrote nothing");
+  if (faults & tq::kFaultIndex)
+    return fail(TQ_EINVAL, "tq_check: a paged call met a slot, page or length outside its cache; it was skipped");
   return TQ_OK;
 }
 

@@ -1,0 +1,313 @@
+// Paged cache write and read-back for sm_100a: rotary positions on several
+// axes, the 4-bit TurboQuant_mse records of the batch's K and V rows written
+// at their slots, and cached rows reconstructed from their slots.
+//
+// Append, per row (one head of one token): K and Q pairs (x1, x2) turn by
+// theta_i = position[axis_i] * inv_freq_i; Q is rounded to its type and
+// stored; K goes on in fp32 (no rounding in between).  Then, for K and V, the
+// canonical encode ("TurboQuant của Google: nén KV cache 6 lần", sections
+// "Trick đầu tiên" and "Lloyd-Max quantizer"): norm, sign flips + FWHT, scale,
+// nearest of 16 levels, packed nibbles -- the same fp32 steps in the same
+// order as tq_encode, so without positions the records are bit-identical.
+//
+// Work layout: a block takes a few tokens; D/16 lanes hold a row, 16
+// coordinates each, so a warp works on 512/D rows of one kind (Q, K or V) at
+// a time.  The block first forms cos and sin of its tokens' angles once for
+// all heads, laid out per coordinate in the order the lanes read them.  The
+// angle is formed in double as a number of turns and only its fraction goes
+// on in fp32, so positions up to 2^31 keep their phase.
+// A pair's other half comes from the row itself through L1 when it lies in
+// another lane (pairs half a head apart).
+
+#include "../../include/tq.h"
+#include "tq_device.cuh"
+#include "tq_paged.h"
+
+namespace tq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxTokens = 4;  // tokens per block
+constexpr int E = 16;          // coordinates per lane
+
+struct AppendParams {
+  PagedAppendArgs a;
+  int tokens;          // tokens per block
+  int gq, gk;          // warp groups per block: of Q rows, of K (and of V) rows
+  unsigned *faults;
+};
+
+__device__ __forceinline__ void store16(void *dst, int dt, const float (&v)[E]) {
+  if (dt == TQ_F32) {
+    float4 *o = static_cast<float4 *>(dst);
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    return;
+  }
+  uint32_t w[E / 2];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    if (dt == TQ_BF16) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    } else {
+      const __half2 b = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+  }
+  uint4 *o = static_cast<uint4 *>(dst);
+  o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <int D, int DT>
+__global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendParams p) {
+  constexpr int T = D / E;           // lanes per row
+  constexpr int RPW = 32 / T;        // rows per warp
+  constexpr int ES = DT == TQ_F32 ? 4 : 2;
+  // (cos, signed sin) per coordinate: chunk c of 4 coordinates of lane t at
+  // float4 c * T + t, so the lanes of a row read consecutive 16-byte words
+  __shared__ float4 s_cos[kMaxTokens][D / 4], s_sin[kMaxTokens][D / 4];
+  __shared__ int64_t s_krec[kMaxTokens], s_vrec[kMaxTokens];  // record of head 0, or -1
+  __shared__ uint32_t s_sign[2][D / 32];
+
+  const PagedAppendArgs &a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t tok0 = (int64_t)blockIdx.x * p.tokens;
+  const int ntok = (int)min((int64_t)p.tokens, a.T - tok0);
+
+  if (warp < 2) {  // sign-flip masks, one ballot per 32 coordinates
+    const int8_t *signs = warp == 0 ? a.kq.signs : a.vq.signs;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      const unsigned m = __ballot_sync(dev::kFull, signs[32 * w + lane] < 0);
+      if (lane == 0) s_sign[warp][w] = m;
+    }
+  }
+  if (tid >= kThreads - kMaxTokens) {
+    const int k = tid - (kThreads - kMaxTokens);
+    if (k < ntok) {
+      const int64_t slot = a.slots[tok0 + k];
+      int64_t kr = -1, vr = -1;
+      if (slot >= a.n_slots) {
+        if (blockIdx.y == 0) atomicOr(p.faults, kFaultIndex);
+      } else if (slot >= 0) {
+        const int64_t page = slot / a.page_size, off = slot - page * a.page_size;
+        kr = page * a.kc.sb + off * a.kc.sn;
+        vr = page * a.vc.sb + off * a.vc.sn;
+      }
+      s_krec[k] = kr;
+      s_vrec[k] = vr;
+    }
+  }
+  const int half = a.rot_dim / 2;
+  for (int i = tid; i < ntok * half; i += kThreads) {
+    const int k = i / half, f = i - k * half;
+    const int ax = a.axis ? min(max(__ldg(a.axis + f), 0), a.n_axes - 1) : 0;
+    const int pos = a.positions[ax * a.pos_stride + tok0 + k];
+    double turns = (double)pos * (double)__ldg(a.inv_freq + f) * 0.15915494309189533577;
+    turns -= rint(turns);
+    float sn, cs;
+    sincospif((float)(2.0 * turns), &sn, &cs);
+    const int i0 = a.adjacent ? 2 * f : f, i1 = a.adjacent ? 2 * f + 1 : f + half;
+    auto at = [&](float4 *s, int c) -> float & {
+      return reinterpret_cast<float *>(s + ((c % E) / 4) * T + c / E)[c & 3];
+    };
+    at(s_cos[k], i0) = cs;
+    at(s_cos[k], i1) = cs;
+    at(s_sin[k], i0) = -sn;
+    at(s_sin[k], i1) = sn;
+  }
+  __syncthreads();
+
+  const int t = lane % T, rw = lane / T;
+  const int groups = p.gq + 2 * p.gk;
+  for (int g = blockIdx.y * kWarps + warp; g < groups; g += gridDim.y * kWarps) {
+    const int kind = g < p.gq ? 0 : g < p.gq + p.gk ? 1 : 2;  // Q, K, V
+    const int H = kind == 0 ? a.Hq : a.Hkv;
+    int row = (g - (kind == 0 ? 0 : kind == 1 ? p.gq : p.gq + p.gk)) * RPW + rw;
+    const bool active = row < ntok * H;
+    if (!active) row = 0;  // idle lanes still take part in the shuffles
+    const int k = row / H, h = row - k * H;
+    const int64_t tok = tok0 + k;
+    const char *src;
+    if (kind == 0)
+      src = static_cast<const char *>(a.q) + (tok * a.q_st + h * a.q_sh) * ES;
+    else if (kind == 1)
+      src = static_cast<const char *>(a.k) + (tok * a.k_st + h * a.k_sh) * ES;
+    else
+      src = static_cast<const char *>(a.v) + (tok * a.v_st + h * a.v_sh) * ES;
+    float x[E];
+    dev::load_block<DT, E>(src + t * E * ES, x);
+
+    if (kind != 2 && t * E < a.rot_dim) {
+      float y[E];  // each coordinate's partner
+      if (a.adjacent) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) y[i] = x[i ^ 1];
+      } else {
+        // half is a multiple of 8, so a chunk of 8 lies on one side of it
+#pragma unroll
+        for (int c = 0; c < E / 8; ++c) {
+          const int i = t * E + 8 * c;
+          const int j = i < half ? i + half : i < a.rot_dim ? i - half : i;
+          float z[8];
+          dev::load_block<DT, 8>(src + j * ES, z);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[8 * c + e] = z[e];
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < E / 4; ++c) {
+        // rot_dim is a multiple of 16: a lane's block is turned or not
+        const float4 cs = s_cos[k][c * T + t], sn = s_sin[k][c * T + t];
+        x[4 * c] = fmaf(x[4 * c], cs.x, y[4 * c] * sn.x);
+        x[4 * c + 1] = fmaf(x[4 * c + 1], cs.y, y[4 * c + 1] * sn.y);
+        x[4 * c + 2] = fmaf(x[4 * c + 2], cs.z, y[4 * c + 2] * sn.z);
+        x[4 * c + 3] = fmaf(x[4 * c + 3], cs.w, y[4 * c + 3] * sn.w);
+      }
+    }
+    if (kind == 0) {
+      if (active)
+        store16(static_cast<char *>(a.q_out) + ((tok * a.Hq + h) * D + t * E) * (int64_t)ES, DT, x);
+      continue;
+    }
+
+    // the canonical encode (tq_encode.cu), 16 levels
+    const QuantParams &q = kind == 1 ? a.kq : a.vq;
+    uint32_t P[8];
+#pragma unroll
+    for (int m = 0; m < 7; ++m) P[m] = __float_as_uint(__ldg(q.thresholds + 8 + m));
+    P[7] = 0;
+    const float nrm = __fsqrt_rn(dev::fold_halves_sumsq<T, E>(x));
+    const uint32_t sw = s_sign[kind - 1][t * E / 32] >> ((t * E) & 31);
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = __uint_as_float(__float_as_uint(x[i]) ^ (((sw >> i) & 1u) << 31));
+    dev::fwht<T, E>(x, t);
+    const float wsc = __fmul_rn(nrm, q.sqrt_d);
+    const float inv = wsc > 0.0f ? __frcp_rn(wsc) : 0.0f;
+    dev::scale_x2<E>(x, inv);
+    uint32_t W[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < E; ++i) dev::put_field<4>(W, i, (uint32_t)dev::quantize_sym<4>(x[i], P));
+    const CacheView &c = kind == 1 ? a.kc : a.vc;
+    const int64_t base = kind == 1 ? s_krec[k] : s_vrec[k];
+    if (active && base >= 0) {
+      const int64_t rec = base + h * c.sh;
+      *reinterpret_cast<uint2 *>(c.codes + rec * (D / 2) + t * 8) = make_uint2(W[0], W[1]);
+      if (t == 0) c.norms[rec] = nrm;
+    }
+  }
+}
+
+struct ReadParams {
+  PagedDequantArgs a;
+  unsigned *faults;
+};
+
+// x_hat = n sigma H(c[idx]) / sqrt(d) of the record at each row's slot; zeros
+// for a row without one.
+template <int D>
+__global__ void __launch_bounds__(kThreads) paged_dequant_kernel(ReadParams p) {
+  constexpr int T = D / E, RPW = 32 / T;
+  __shared__ float s_cent[16];
+  __shared__ uint32_t s_sign[D / 32];
+  const PagedDequantArgs &a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < 16) s_cent[tid] = a.q.centroids[tid];
+  if (warp == 1) {
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      const unsigned m = __ballot_sync(dev::kFull, a.q.signs[32 * w + lane] < 0);
+      if (lane == 0) s_sign[w] = m;
+    }
+  }
+  __syncthreads();
+  const int t = lane % T;
+  const int64_t rows = a.T * a.H;
+  const int64_t step = (int64_t)gridDim.x * kWarps * RPW;
+  for (int64_t r0 = ((int64_t)blockIdx.x * kWarps + warp) * RPW; r0 < rows; r0 += step) {
+    int64_t row = r0 + lane / T;
+    const bool active = row < rows;
+    if (!active) row = r0;
+    const int64_t tok = row / a.H;
+    const int h = (int)(row - tok * a.H);
+    const int64_t slot = a.slots[tok];
+    int64_t rec = -1;
+    if (slot >= a.n_slots) {
+      if (t == 0 && h == 0) atomicOr(p.faults, kFaultIndex);
+    } else if (slot >= 0) {
+      const int64_t page = slot / a.page_size;
+      rec = page * a.c.sb + (slot - page * a.page_size) * a.c.sn + h * a.c.sh;
+    }
+    float x[E], sc = 0.f;
+    uint32_t W[2] = {0u, 0u};
+    if (rec >= 0) {
+      dev::load_words<2>(a.c.codes + rec * (D / 2) + t * 8, W);
+      sc = __fdiv_rn(__ldg(a.c.norms + rec), a.q.sqrt_d);
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = s_cent[dev::get_field<4>(W, i)];
+    dev::fwht<T, E>(x, t);
+    const uint32_t sw = s_sign[t * E / 32] >> ((t * E) & 31);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float y = __uint_as_float(__float_as_uint(x[i]) ^ (((sw >> i) & 1u) << 31));
+      x[i] = rec >= 0 ? y * sc : 0.f;
+    }
+    if (active)
+      store16(static_cast<char *>(a.out) + (row * D + t * E) * (a.out_dtype == TQ_F32 ? 4 : 2), a.out_dtype, x);
+  }
+}
+
+template <int D>
+cudaError_t append_d(const AppendParams &p, dim3 grid, cudaStream_t s) {
+  switch (p.a.dtype) {
+    case TQ_F32: paged_append_kernel<D, TQ_F32><<<grid, kThreads, 0, s>>>(p); break;
+    case TQ_BF16: paged_append_kernel<D, TQ_BF16><<<grid, kThreads, 0, s>>>(p); break;
+    default: paged_append_kernel<D, TQ_F16><<<grid, kThreads, 0, s>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedAppendArgs &a, cudaStream_t s) {
+  AppendParams p{a, 1, 0, 0, nullptr};
+  cudaError_t e = fault_word(&p.faults);
+  if (e != cudaSuccess) return e;
+  const int rpw = 512 / a.kq.d, sms = decode_ctas();
+  // more tokens to a block once that still leaves a few blocks an SM
+  while (p.tokens < kMaxTokens && a.T / (2 * p.tokens) >= 4 * sms) p.tokens *= 2;
+  p.gq = (p.tokens * a.Hq + rpw - 1) / rpw;
+  p.gk = (p.tokens * a.Hkv + rpw - 1) / rpw;
+  const int64_t bx = (a.T + p.tokens - 1) / p.tokens;
+  // few tokens: their rows spread over several blocks
+  const int most = (p.gq + 2 * p.gk + kWarps - 1) / kWarps;
+  const int by = (int)max((int64_t)1, min((int64_t)most, (2 * sms + bx - 1) / bx));
+  const dim3 grid((unsigned)bx, (unsigned)by);
+  switch (a.kq.d) {
+    case 64: return append_d<64>(p, grid, s);
+    case 128: return append_d<128>(p, grid, s);
+    case 256: return append_d<256>(p, grid, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_paged_dequant(const PagedDequantArgs &a, cudaStream_t s) {
+  ReadParams p{a, nullptr};
+  cudaError_t e = fault_word(&p.faults);
+  if (e != cudaSuccess) return e;
+  const int rpb = kWarps * (512 / a.q.d);
+  const int64_t blocks = min((a.T * a.H + rpb - 1) / rpb, (int64_t)decode_ctas() * 16);
+  switch (a.q.d) {
+    case 64: paged_dequant_kernel<64><<<(unsigned)blocks, kThreads, 0, s>>>(p); break;
+    case 128: paged_dequant_kernel<128><<<(unsigned)blocks, kThreads, 0, s>>>(p); break;
+    case 256: paged_dequant_kernel<256><<<(unsigned)blocks, kThreads, 0, s>>>(p); break;
+    default: return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace tq
