@@ -192,18 +192,16 @@ cudaError_t run_general(const GeneralParams &p, cudaStream_t s) {
 
 }  // namespace
 
-size_t paged_attention_workspace(int R, int64_t T, int Hq, int Hkv, int d) { return 16; }
+size_t paged_attention_workspace(int R, int64_t T, int Hq, int Hkv, int d) {
+  return d == 256 ? 16 : paged_rows_workspace(d);
+}
 
 cudaError_t launch_paged_attention(const PagedAttentionArgs &a, cudaStream_t s) {
+  if (a.kq.d != 256) return launch_paged_rows(a, s);
   GeneralParams p{a, nullptr};
   const cudaError_t e = fault_word(&p.faults);
   if (e != cudaSuccess) return e;
-  switch (a.kq.d) {
-    case 64: return run_general<64>(p, s);
-    case 128: return run_general<128>(p, s);
-    case 256: return run_general<256>(p, s);
-  }
-  return cudaErrorInvalidValue;
+  return run_general<256>(p, s);
 }
 
 }  // namespace tq
