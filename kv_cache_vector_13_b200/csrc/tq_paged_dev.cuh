@@ -16,6 +16,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // A factor s in [1, 2) whose products s c_k round to fp16 with the smallest
 // worst relative error over the 16 levels, out of 32 candidates (ties to the
 // smaller one).  The whole warp calls it; every lane gets s.  A single

@@ -8,20 +8,19 @@
 // a range's end leave partial sums that a second kernel merges, in the order
 // of the tokens, so the result does not depend on timing.
 //
-// A step of a warp: S = Q K^T with mma.m16n8k16 (fp16, fp32 sums), the
-// running softmax, O += P V.  A tile has 8 query rows, each as the fp16 pair
-// hi + lo in rows g and g + 8 of the 16-row operand (S and O are the sums of
-// the two), or 16 rows rounded once.  Codes become operand words without
-// arithmetic: a code byte (two codes) indexes a 256-entry table of fp16
-// centroid pairs, one copy per lane, placed so that one byte permute forms
-// the shared address.  For K the pair is two coordinates of a token; for V
-// the codes of two tokens are first interleaved, so the pair is two tokens at
-// one coordinate.  The order of coordinates within the products is free, so
-// every lane loads whole 16-byte (K) and 8-byte (V) runs of a record.
-// Norms enter behind the products: ||k|| scales the logit, ||v|| the weight.
-//
-// What bounds it: table reads, 64 a lane per step (a 128-byte read per clock
-// and SM), about 16 warp instructions per token and KV head.
+// A step of a warp: S^T = K Q^T and O^T += V^T P^T with mma.m16n8k16 (fp16,
+// fp32 sums), the tokens (then the coordinates) being the 16 rows and the
+// query rows the 8 columns, and the running softmax in between.  Query rows
+// and weights are carried as fp16 pairs hi + lo: up to 4 rows a tile put both
+// into one product, as columns g and g + 4 (S and O are the sums of the two);
+// up to 8 take two products into the same sums.  Codes become operand words
+// without arithmetic: a code byte (two codes) indexes a 256-entry table of
+// fp16 centroid pairs, one copy per lane, placed so that one byte permute
+// forms the shared address.  For K the pair is two coordinates of a token; for
+// V the codes of two tokens are first interleaved, so the pair is two tokens
+// at one coordinate.  The order of coordinates within the products is free, so
+// every lane loads whole 16-byte (K) and 8-byte (V) runs of a record.  Norms
+// enter behind the products: ||k|| scales the logit, ||v|| the weight.
 
 #include "../../include/tq.h"
 #include "tq_device.cuh"
@@ -29,6 +28,8 @@
 #include "tq_paged_dev.cuh"
 
 #include <float.h>
+
+#include <type_traits>
 
 namespace tq {
 namespace {
@@ -38,11 +39,11 @@ using namespace paged;
 constexpr int kStep = 16;                // tokens per step
 constexpr uint32_t kTabAddr = 0x10000u;  // the pair tables: 64 KiB at this shared address
 constexpr uint32_t kPartAddr = 0x20000u; // the warps' partial sums
-constexpr int kMaxRows = 16;
+constexpr int kMaxRows = 8;
 
 template <int D>
 struct Cfg {
-  static constexpr int kWarps = D == 128 ? 12 : 16;
+  static constexpr int kWarps = 16;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kPitch = D + 4;  // floats of a partial row (no bank clash between rows)
 };
@@ -52,15 +53,15 @@ template <int D>
 struct Low {
   int64_t base[Cfg<D>::kThreads];  // the line at each thread's first request
   int64_t warp[Cfg<D>::kWarps];
-  __half q[2][8][D + 8];           // operand rows g and g + 8
+  __half q[2][8][D + 8];           // operand columns: hi of each row, lo of each row
   float f[kMaxRows];               // logit factor of each row
   float m[Cfg<D>::kWarps][kMaxRows], l[Cfg<D>::kWarps][kMaxRows];
   float scale[2];                  // the tables' scales
 };
 
-template <int D, bool HILO>
+template <int D>
 __host__ __device__ constexpr uint32_t smem_end() {
-  return kPartAddr + Cfg<D>::kWarps * (HILO ? 8 : 16) * Cfg<D>::kPitch * 4;
+  return kPartAddr + Cfg<D>::kWarps * kMaxRows * Cfg<D>::kPitch * 4;
 }
 
 struct RowsParams {
@@ -118,12 +119,19 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Transpose of an 8 x 8 matrix of 16-bit values, two of row lane / 4 a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // Codes and norms of one step as a lane needs them.
 template <int D>
 struct Codes {
   uint32_t k[2][D / 32];  // tokens g and 8 + g, coordinates [q D/4, (q + 1) D/4)
   uint32_t v[4][D / 64];  // tokens 2q, 2q+1, 8+2q, 9+2q, coordinates [g D/8, (g + 1) D/8)
-  float kn[4], vn[4];     // tokens 2q, 2q+1, 8+2q, 9+2q
+  float kn[2], vn[2];     // tokens g and 8 + g
 };
 
 template <int N>
@@ -139,12 +147,15 @@ __device__ __forceinline__ void ldg_words(const uint8_t *p, uint32_t (&w)[N]) {
   }
 }
 
-template <int D, bool HILO>
+// P4: up to 4 query rows a tile, hi and lo in one product; else up to 8.
+// UNIT: the tokens of a page lie side by side.
+template <int D, bool P4, bool UNIT>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr int W = Cfg<D>::kWarps, NT = Cfg<D>::kThreads, PITCH = Cfg<D>::kPitch;
-  constexpr int RT = HILO ? 8 : 16;  // query rows per tile
-  constexpr int KS = D / 16;         // k steps of the scores
-  constexpr int NV = D / 8;          // n tiles of the values
+  constexpr int RT = P4 ? 4 : 8;  // query rows per tile
+  constexpr int KS = D / 16;      // k steps of the scores
+  constexpr int MV = D / 16;      // m tiles of the values
+  constexpr int QS = P4 ? 1 : 2;  // products per step
   extern __shared__ __align__(16) unsigned char s_raw[];
   Low<D> &sm = *reinterpret_cast<Low<D> *>(s_raw);
   auto &s_base = sm.base;
@@ -162,7 +173,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
   const uint32_t dyn = (uint32_t)__cvta_generic_to_shared(s_raw);
   uint32_t dyn_bytes;
   asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn_bytes));
-  if (dyn + sizeof(Low<D>) > kTabAddr || dyn + dyn_bytes < smem_end<D, HILO>()) {
+  if (dyn + sizeof(Low<D>) > kTabAddr || dyn + dyn_bytes < smem_end<D>()) {
     if (tid == 0) {
       atomicOr(p.faults, kFaultSmemLayout);
       p.desc[c] = make_int4(0, 0, 0, 0);
@@ -243,8 +254,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
   const uint32_t ktab = kTabAddr + 4 * lane, vtab = ktab + 128;
   const float kscale = a.scale * 1.4426950408889634f / (a.kq.sqrt_d * s_scale[0]);
   const float vscale = 1.0f / (a.vq.sqrt_d * s_scale[1]);
-  const bool pairs_ok = a.k.sn == 1 && a.v.sn == 1 && ((a.k.sb | a.k.sh | a.v.sb | a.v.sh) & 1) == 0 &&
-                        (((uintptr_t)a.k.norms | (uintptr_t)a.v.norms) & 7) == 0;
 
   while (at < end && r < a.R) {
     // ---- the piece: steps [s0, s1) of unit (r, h, tile)
@@ -275,27 +284,26 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
       for (int e = 0; e < D / 32; ++e) {
         const float y = v[e] * f;
         const __half hi = __float2half_rn(y);
-        s_q[HILO ? 0 : i >> 3][i & 7][lane * (D / 32) + e] = hi;
-        if (HILO) s_q[1][i][lane * (D / 32) + e] = __float2half_rn(y - __half2float(hi));
+        s_q[0][i][lane * (D / 32) + e] = hi;
+        s_q[P4 ? 0 : 1][P4 ? i + 4 : i][lane * (D / 32) + e] = __float2half_rn(y - __half2float(hi));
       }
     }
     __syncthreads();
-    uint32_t qa[KS][4];
+    uint32_t qb[QS][KS][2];
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
+    for (int o = 0; o < QS; ++o)
 #pragma unroll
-      for (int o = 0; o < 2; ++o) {
+      for (int s = 0; s < KS; ++s) {
         const uint2 t = *reinterpret_cast<const uint2 *>(&s_q[o][g][q4 * (D / 4) + 4 * s]);
-        qa[s][o] = t.x;
-        qa[s][2 + o] = t.y;
+        qb[o][s][0] = t.x;
+        qb[o][s][1] = t.y;
       }
-    // what each of the lane's rows sees; rows that are not there see everything (and go nowhere)
-    constexpr int LR = HILO ? 1 : 2;
-    int see_lo[LR], see_hi[LR];
-    float f[LR], M[LR], l[LR];
+    // the lane's two rows; one that is not there sees everything (and goes nowhere)
+    int see_lo[2], see_hi[2];
+    float f[2], M[2], l[2];
 #pragma unroll
-    for (int o = 0; o < LR; ++o) {
-      const int i = g + 8 * o;
+    for (int o = 0; o < 2; ++o) {
+      const int i = (2 * q4 + o) & (RT - 1);
       see_lo[o] = 0;
       see_hi[o] = INT_MAX;
       if (i < nrows) {
@@ -312,171 +320,203 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
     const int full_hi = a.causal ? max(first_pos + 1, 0) : req.kv;
     const int full_lo = a.window > 0 ? max(last_pos + 1 - a.window, 0) : 0;
 
-    float acc[NV][4];
+    float acc[MV][4];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < MV; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 
     const int32_t *row = a.table + (int64_t)r * a.table_stride;
-    // records of the warp's next 32 steps, one a lane: -1 without a page
-    int64_t krec = -1, vrec = -1;
     const int n_steps = s1 - s0 > warp ? (s1 - s0 - warp + W - 1) / W : 0;
-    auto fetch_pages = [&](int it) {
-      const int s = s0 + warp + (it + lane) * W;
-      krec = vrec = -1;
+    // The records of 8 of the warp's steps, step it + lane % 8 a lane; -1 without a page.  They are found a
+    // batch ahead and brought into L2 (lane / 8: codes and norms of K and of V).
+    int64_t krec, vrec, krec2, vrec2;
+    auto find = [&](int it, int64_t &kr, int64_t &vr) {
+      const int s = s0 + warp + (it + (lane & 7)) * W;
+      kr = vr = -1;
       const int t0 = s * kStep;
       if (s < s1 && t0 < req.kv) {
         const int page = t0 / a.page_size, off = t0 - page * a.page_size;
         const int id = __ldg(row + page);
         if ((unsigned)id < (unsigned)a.n_pages) {
-          krec = id * a.k.sb + h * a.k.sh + off * a.k.sn;
-          vrec = id * a.v.sb + h * a.v.sh + off * a.v.sn;
+          kr = id * a.k.sb + h * a.k.sh + off * a.k.sn;
+          vr = id * a.v.sb + h * a.v.sh + off * a.v.sn;
         } else {
           atomicOr(p.faults, kFaultIndex);
         }
       }
     };
+    auto warm = [&](int64_t kr, int64_t vr) {
+      if (!UNIT || kr < 0) return;
+      const int what = lane >> 3;
+      const bool norm = what & 1;
+      const char *at = norm ? reinterpret_cast<const char *>((what & 2 ? a.v.norms : a.k.norms) + (what & 2 ? vr : kr))
+                            : reinterpret_cast<const char *>((what & 2 ? a.v.codes : a.k.codes) + (what & 2 ? vr : kr) * (D / 2));
+      // a run of norms may begin inside a 16-byte word: the words that hold it
+      const uintptr_t lo = (uintptr_t)at & ~(uintptr_t)15;
+      const uint32_t n = norm ? (uint32_t)(((uintptr_t)at + 4 * kStep + 15 - lo) & ~(uintptr_t)15) : kStep * (D / 2);
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(lo), "r"(n) : "memory");
+    };
     auto load_k = [&](int64_t kr, Codes<D> &cd) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        ldg_words(a.k.codes + (kr + (8 * i + g) * a.k.sn) * (D / 2) + q4 * (D / 8), cd.k[i]);
-      if (pairs_ok) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float2 t = __ldg(reinterpret_cast<const float2 *>(a.k.norms + kr + 8 * i + 2 * q4));
-          cd.kn[2 * i] = t.x;
-          cd.kn[2 * i + 1] = t.y;
-        }
+      if constexpr (UNIT) {
+        const uint8_t *c = a.k.codes + kr * (D / 2) + (g * (D / 2) + q4 * (D / 8));
+        ldg_words(c, cd.k[0]);
+        ldg_words(c + 8 * (D / 2), cd.k[1]);
+        const float *n = a.k.norms + kr + g;
+        cd.kn[0] = __ldg(n);
+        cd.kn[1] = __ldg(n + 8);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cd.kn[i] = __ldg(a.k.norms + kr + (8 * (i >> 1) + 2 * q4 + (i & 1)) * a.k.sn);
+        for (int i = 0; i < 2; ++i) {
+          ldg_words(a.k.codes + (kr + (8 * i + g) * a.k.sn) * (D / 2) + q4 * (D / 8), cd.k[i]);
+          cd.kn[i] = __ldg(a.k.norms + kr + (8 * i + g) * a.k.sn);
+        }
       }
     };
     auto load_v = [&](int64_t vr, Codes<D> &cd) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        ldg_words(a.v.codes + (vr + (8 * (i >> 1) + 2 * q4 + (i & 1)) * a.v.sn) * (D / 2) + g * (D / 16), cd.v[i]);
-      if (pairs_ok) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float2 t = __ldg(reinterpret_cast<const float2 *>(a.v.norms + vr + 8 * i + 2 * q4));
-          cd.vn[2 * i] = t.x;
-          cd.vn[2 * i + 1] = t.y;
-        }
+      if constexpr (UNIT) {
+        const uint8_t *c = a.v.codes + vr * (D / 2) + (q4 * D + g * (D / 16));
+        ldg_words(c, cd.v[0]);
+        ldg_words(c + D / 2, cd.v[1]);
+        ldg_words(c + 8 * (D / 2), cd.v[2]);
+        ldg_words(c + 9 * (D / 2), cd.v[3]);
+        const float *n = a.v.norms + vr + g;
+        cd.vn[0] = __ldg(n);
+        cd.vn[1] = __ldg(n + 8);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cd.vn[i] = __ldg(a.v.norms + vr + (8 * (i >> 1) + 2 * q4 + (i & 1)) * a.v.sn);
+        for (int i = 0; i < 4; ++i)
+          ldg_words(a.v.codes + (vr + (8 * (i >> 1) + 2 * q4 + (i & 1)) * a.v.sn) * (D / 2) + g * (D / 16), cd.v[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) cd.vn[i] = __ldg(a.v.norms + vr + (8 * i + g) * a.v.sn);
+      }
+    };
+    // The running softmax of the lane's rows over its tokens g and 8 + g (value 2 i + o: token 8 i + g, row o):
+    // scores in, weights times value norms out.  M is a reference that moves only when one of them would pass 2^8.
+    auto soft = [&](auto edge, int t0, float (&t)[4], const Codes<D> &cd) {
+      constexpr bool EDGE = decltype(edge)::value;
+      float lv[2], mx[2], s[4];
+      bool seen[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = t0 + 8 * i + g;
+        lv[i] = fmaxf(log2_approx(cd.vn[i]), -64.f);
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          const int e = 2 * i + o;
+          seen[e] = !EDGE || (j >= see_lo[o] && j < see_hi[o] && j < req.kv);
+          s[e] = t[e] * (f[o] * cd.kn[i]);
+          t[e] = s[e] - M[o];
+          if (EDGE && !seen[e]) t[e] = -INFINITY;
+        }
+      }
+      if (__any_sync(dev::kFull, fmaxf(fmaxf(t[0], t[1]) + lv[0], fmaxf(t[2], t[3]) + lv[1]) > 8.f)) {
+        float r2[2];
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          mx[o] = fmaxf(seen[o] ? s[o] + lv[0] : -INFINITY, seen[2 + o] ? s[2 + o] + lv[1] : -INFINITY);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) mx[o] = fmaxf(mx[o], __shfl_xor_sync(dev::kFull, mx[o], x));
+          const float m2 = fmaxf(M[o], mx[o]);
+          r2[o] = exp2f(M[o] - m2);
+          M[o] = m2;
+          l[o] *= r2[o];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) t[2 * i + o] = seen[2 * i + o] ? s[2 * i + o] - m2 : -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < MV; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][e] *= r2[e & 1];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        t[e] = exp2_approx(t[e]);
+        l[e & 1] += t[e];
+        t[e] *= cd.vn[e >> 1];
+        if (EDGE && !seen[e]) t[e] = 0.f;
       }
     };
 
     Codes<D> cd;
-    int64_t kr = -1, vr = -1;
+    bool have = false;  // the step has a page
     if (n_steps > 0) {
-      fetch_pages(0);
-      kr = __shfl_sync(dev::kFull, krec, 0);
-      vr = __shfl_sync(dev::kFull, vrec, 0);
-      if (kr >= 0) {
+      find(0, krec, vrec);
+      warm(krec, vrec);
+      find(8, krec2, vrec2);
+      const int64_t kr = __shfl_sync(dev::kFull, krec, 0), vr = __shfl_sync(dev::kFull, vrec, 0);
+      have = kr >= 0;
+      if (have) {
         load_k(kr, cd);
         load_v(vr, cd);
       }
     }
     for (int it = 0; it < n_steps; ++it) {
-      const bool have = kr >= 0;
       const int t0 = (s0 + warp + it * W) * kStep;
-      // the next step's records
-      int64_t nkr = -1, nvr = -1;
-      if (it + 1 < n_steps) {
-        if (((it + 1) & 31) == 0) fetch_pages(it + 1);
-        nkr = __shfl_sync(dev::kFull, krec, (it + 1) & 31);
-        nvr = __shfl_sync(dev::kFull, vrec, (it + 1) & 31);
+      if ((it & 7) == 3) warm(krec2, vrec2);
+      if ((it & 7) == 7) {
+        krec = krec2;
+        vrec = vrec2;
+        find(it + 9, krec2, vrec2);
       }
+      // find() gives -1 behind the piece's last step
       if (!have) {
-        kr = nkr;
-        vr = nvr;
-        if (kr >= 0) {
+        const int64_t kr = __shfl_sync(dev::kFull, krec, (it + 1) & 7);
+        const int64_t vr = __shfl_sync(dev::kFull, vrec, (it + 1) & 7);
+        have = kr >= 0;
+        if (have) {
           load_k(kr, cd);
           load_v(vr, cd);
         }
         continue;
       }
-      // ---- scores of tokens 8 i + 2 q4 + {0, 1}
+      // ---- scores: value 2 i + o is token 8 i + g, column 2 q4 + o
       float sc[2][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int c2 = 0; c2 < 2; ++c2)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[i][e] = 0.f;
+        for (int e = 0; e < 4; ++e) sc[c2][e] = 0.f;
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-          const uint32_t u = cd.k[i][w];
-          mma(sc[i], qa[2 * w][0], qa[2 * w][1], qa[2 * w][2], qa[2 * w][3], pair<0>(u, ktab), pair<1>(u, ktab));
-          mma(sc[i], qa[2 * w + 1][0], qa[2 * w + 1][1], qa[2 * w + 1][2], qa[2 * w + 1][3], pair<2>(u, ktab),
-              pair<3>(u, ktab));
+      for (int w = 0; w < D / 32; ++w) {
+        const uint32_t x = cd.k[0][w], y = cd.k[1][w];
+        const uint32_t a0 = pair<0>(x, ktab), a1 = pair<0>(y, ktab), a2 = pair<1>(x, ktab), a3 = pair<1>(y, ktab);
+        const uint32_t b0 = pair<2>(x, ktab), b1 = pair<2>(y, ktab), b2 = pair<3>(x, ktab), b3 = pair<3>(y, ktab);
+#pragma unroll
+        for (int o = 0; o < QS; ++o) {
+          // two chains of sums
+          mma(sc[0], a0, a1, a2, a3, qb[o][2 * w][0], qb[o][2 * w][1]);
+          mma(sc[1], b0, b1, b2, b3, qb[o][2 * w + 1][0], qb[o][2 * w + 1][1]);
         }
       }
-      float kn[4];
+      float t[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) kn[e] = cd.kn[e];
-      if (nkr >= 0) load_k(nkr, cd);
-      // ---- softmax; M is a reference that moves only when a weight times its norm would pass 2^8
-      const bool edge = t0 + kStep > full_hi || t0 < full_lo;
-      float lv[4];
+      for (int e = 0; e < 4; ++e) {
+        t[e] = sc[0][e] + sc[1][e];
+        if (P4) t[e] += __shfl_xor_sync(dev::kFull, t[e], 2);  // the hi and lo columns
+      }
+      if (t0 + kStep > full_hi || t0 < full_lo)
+        soft(std::true_type{}, t0, t, cd);
+      else
+        soft(std::false_type{}, t0, t, cd);
+      // weights to operand words: fp16 pairs of two rows at a token, transposed to two tokens of a row
+      uint32_t pb[QS][2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) lv[e] = fmaxf(__log2f(cd.vn[e]), -64.f);
-      uint32_t pa[4];
-#pragma unroll
-      for (int o = 0; o < LR; ++o) {
-        float z[4], t[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          z[e] = HILO ? sc[e >> 1][e & 1] + sc[e >> 1][2 + (e & 1)] : sc[e >> 1][2 * o + (e & 1)];
-          z[e] *= f[o] * kn[e];
+      for (int i = 0; i < 2; ++i) {
+        const __half2 hi = __floats2half2_rn(t[2 * i], t[2 * i + 1]);
+        const float2 back = __half22float2(hi);
+        const __half2 lo = __floats2half2_rn(t[2 * i] - back.x, t[2 * i + 1] - back.y);
+        const uint32_t wh = *reinterpret_cast<const uint32_t *>(&hi), wl = *reinterpret_cast<const uint32_t *>(&lo);
+        if (P4) {
+          pb[0][i] = transpose8(q4 < 2 ? wh : wl);
+        } else {
+          pb[0][i] = transpose8(wh);
+          pb[QS - 1][i] = transpose8(wl);
         }
-        bool seen[4] = {true, true, true, true};
-        if (edge) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = t0 + 8 * (e >> 1) + 2 * q4 + (e & 1);
-            seen[e] = j >= see_lo[o] && j < see_hi[o] && j < req.kv;
-            if (!seen[e]) z[e] = -INFINITY;
-          }
-        }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, seen[e] ? z[e] + lv[e] : -INFINITY);
-        if (__any_sync(dev::kFull, mx > M[o] + 8.f)) {
-          mx = fmaxf(mx, __shfl_xor_sync(dev::kFull, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(dev::kFull, mx, 2));
-          const float m2 = fmaxf(M[o], mx), s = exp2f(M[o] - m2);
-          M[o] = m2;
-          l[o] *= s;
-#pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            acc[j][2 * o] *= s;
-            acc[j][2 * o + 1] *= s;
-            if (HILO) {
-              acc[j][2] *= s;
-              acc[j][3] *= s;
-            }
-          }
-        }
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          t[e] = exp2_approx(z[e] - M[o]);
-          l[o] += t[e];
-          w[e] = seen[e] ? t[e] * cd.vn[e] : 0.f;
-        }
-        const __half2 h0 = __floats2half2_rn(w[0], w[1]), h1 = __floats2half2_rn(w[2], w[3]);
-        pa[o] = *reinterpret_cast<const uint32_t *>(&h0);
-        pa[2 + o] = *reinterpret_cast<const uint32_t *>(&h1);
-        if (HILO) {
-          const float2 b0 = __half22float2(h0), b1 = __half22float2(h1);
-          const __half2 l0 = __floats2half2_rn(w[0] - b0.x, w[1] - b0.y);
-          const __half2 l1 = __floats2half2_rn(w[2] - b1.x, w[3] - b1.y);
-          pa[1] = *reinterpret_cast<const uint32_t *>(&l0);
-          pa[3] = *reinterpret_cast<const uint32_t *>(&l1);
-        }
+      }
+      {
+        const int64_t kr = __shfl_sync(dev::kFull, krec, (it + 1) & 7);
+        have = kr >= 0;
+        if (have) load_k(kr, cd);
       }
       // ---- values: tokens 2 q4 and 2 q4 + 1 interleaved (even and odd coordinates apart)
 #pragma unroll
@@ -486,37 +526,45 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
         const uint32_t o0 = ((x0 >> 4) & 0x0f0f0f0fu) | (x1 & 0xf0f0f0f0u);
         const uint32_t e1 = (x2 & 0x0f0f0f0fu) | ((x3 << 4) & 0xf0f0f0f0u);
         const uint32_t o1 = ((x2 >> 4) & 0x0f0f0f0fu) | (x3 & 0xf0f0f0f0u);
-        mma(acc[8 * w + 0], pa[0], pa[1], pa[2], pa[3], pair<0>(e0, vtab), pair<0>(e1, vtab));
-        mma(acc[8 * w + 1], pa[0], pa[1], pa[2], pa[3], pair<0>(o0, vtab), pair<0>(o1, vtab));
-        mma(acc[8 * w + 2], pa[0], pa[1], pa[2], pa[3], pair<1>(e0, vtab), pair<1>(e1, vtab));
-        mma(acc[8 * w + 3], pa[0], pa[1], pa[2], pa[3], pair<1>(o0, vtab), pair<1>(o1, vtab));
-        mma(acc[8 * w + 4], pa[0], pa[1], pa[2], pa[3], pair<2>(e0, vtab), pair<2>(e1, vtab));
-        mma(acc[8 * w + 5], pa[0], pa[1], pa[2], pa[3], pair<2>(o0, vtab), pair<2>(o1, vtab));
-        mma(acc[8 * w + 6], pa[0], pa[1], pa[2], pa[3], pair<3>(e0, vtab), pair<3>(e1, vtab));
-        mma(acc[8 * w + 7], pa[0], pa[1], pa[2], pa[3], pair<3>(o0, vtab), pair<3>(o1, vtab));
+        auto tile = [&](auto k) {
+          constexpr int K = decltype(k)::value;
+          const uint32_t a0 = pair<K>(e0, vtab), a1 = pair<K>(o0, vtab), a2 = pair<K>(e1, vtab), a3 = pair<K>(o1, vtab);
+#pragma unroll
+          for (int o = 0; o < QS; ++o) mma(acc[4 * w + K], a0, a1, a2, a3, pb[o][0], pb[o][1]);
+        };
+        tile(std::integral_constant<int, 0>{});
+        tile(std::integral_constant<int, 1>{});
+        tile(std::integral_constant<int, 2>{});
+        tile(std::integral_constant<int, 3>{});
       }
-      if (nvr >= 0) load_v(nvr, cd);
-      kr = nkr;
-      vr = nvr;
+      const int64_t vr = __shfl_sync(dev::kFull, vrec, (it + 1) & 7);
+      if (have) load_v(vr, cd);
     }
 
-    // ---- the warps' sums: coordinate n (D/8) + j of a row at 8 j + n
+    // ---- the warps' sums: coordinate g (D/8) + 2 j + b of a row at 16 j + 2 g + b
 #pragma unroll
-    for (int o = 0; o < LR; ++o) {
+    for (int o = 0; o < 2; ++o) {
       float t = l[o];
-      t += __shfl_xor_sync(dev::kFull, t, 1);
-      t += __shfl_xor_sync(dev::kFull, t, 2);
-      if (q4 == 0) {
-        s_m[warp][g + 8 * o] = M[o];
-        s_l[warp][g + 8 * o] = t;
-      }
-      float *dst = parts + ((size_t)warp * RT + g + 8 * o) * PITCH + 2 * q4;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        *reinterpret_cast<float2 *>(dst + 8 * j) =
-            HILO ? make_float2(acc[j][0] + acc[j][2], acc[j][1] + acc[j][3])
-                 : make_float2(acc[j][2 * o], acc[j][2 * o + 1]);
+      for (int x = 4; x < 32; x <<= 1) t += __shfl_xor_sync(dev::kFull, t, x);
+      if (g == 0 && 2 * q4 < RT) {
+        s_m[warp][2 * q4 + o] = M[o];
+        s_l[warp][2 * q4 + o] = t;
+      }
     }
+#pragma unroll
+    for (int j = 0; j < MV; ++j)
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        float x = acc[j][o], y = acc[j][2 + o];
+        if (P4) {
+          x += __shfl_xor_sync(dev::kFull, x, 2);
+          y += __shfl_xor_sync(dev::kFull, y, 2);
+        }
+        if (2 * q4 < RT)
+          *reinterpret_cast<float2 *>(parts + ((size_t)warp * kMaxRows + 2 * q4 + o) * PITCH + 16 * j + 2 * g) =
+              make_float2(x, y);
+      }
     __syncthreads();
     const bool starts = s0 == req.lo, ends = s1 == req.hi;
     for (int i = warp; i < nrows; i += W) {
@@ -530,11 +578,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
       for (int w = 0; w < W; ++w) {
         const float s = exp2f(s_m[w][i] - m);
         L += s * s_l[w][i];
-        const float *src = parts + ((size_t)w * RT + i) * PITCH;
+        const float *src = parts + ((size_t)w * kMaxRows + i) * PITCH;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
-          const int k = lane * (D / 32) + e;
-          y[e] = fmaf(s, src[8 * (k % NV) + k / NV], y[e]);
+          const int k = lane * (D / 32) + e, u = k % (D / 8);
+          y[e] = fmaf(s, src[16 * (u / 2) + 2 * (k / (D / 8)) + (u & 1)], y[e]);
         }
       }
       if (starts && ends) {
@@ -573,9 +621,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
 
 // Merges the pieces of the unit that starts last in CTA c's range and goes on
 // behind it, a warp a row, in the order of the tokens.
-template <int D, bool HILO>
+template <int D, bool P4>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ RowsParams p) {
-  constexpr int RT = HILO ? 8 : 16;
+  constexpr int RT = P4 ? 4 : 8;
   const PagedAttentionArgs &a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
   const float vs = table_scale(a.vq.centroids, lane);
@@ -610,11 +658,11 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   }
 }
 
-template <int D, bool HILO>
+template <int D, bool P4, bool UNIT>
 cudaError_t run_rows(const RowsParams &p, cudaStream_t s) {
   // dynamic shared memory starts behind the 1 KiB that the system keeps
-  const int dyn = (int)smem_end<D, HILO>() - 1024;
-  auto kern = paged_rows_kernel<D, HILO>;
+  const int dyn = (int)smem_end<D>() - 1024;
+  auto kern = paged_rows_kernel<D, P4, UNIT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
   if (e != cudaSuccess) return e;
   const int ctas = decode_ctas();
@@ -630,7 +678,14 @@ cudaError_t run_rows(const RowsParams &p, cudaStream_t s) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, HILO>, p);
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, P4>, p);
+}
+
+template <int D>
+cudaError_t run_d(const RowsParams &p, bool p4, cudaStream_t s) {
+  const bool unit = p.a.k.sn == 1 && p.a.v.sn == 1;
+  if (p4) return unit ? run_rows<D, true, true>(p, s) : run_rows<D, true, false>(p, s);
+  return unit ? run_rows<D, false, true>(p, s) : run_rows<D, false, false>(p, s);
 }
 
 }  // namespace
@@ -646,9 +701,8 @@ cudaError_t launch_paged_rows(const PagedAttentionArgs &a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   p.desc = static_cast<int4 *>(a.ws);
   p.slots = reinterpret_cast<float *>(p.desc + decode_ctas());
-  const bool hilo = (int64_t)a.max_q * (a.Hq / a.Hkv) <= 8;
-  if (a.kq.d == 64) return hilo ? run_rows<64, true>(p, s) : run_rows<64, false>(p, s);
-  return hilo ? run_rows<128, true>(p, s) : run_rows<128, false>(p, s);
+  const bool p4 = (int64_t)a.max_q * (a.Hq / a.Hkv) <= 4;
+  return a.kq.d == 64 ? run_d<64>(p, p4, s) : run_d<128>(p, p4, s);
 }
 
 }  // namespace tq
