@@ -5,6 +5,7 @@ of libtq_b200.so; torch supplies device memory, strides and the current
 stream.  The names follow the C ABI (include/tq.h).
 """
 
+import contextlib
 import ctypes
 import math
 from dataclasses import dataclass
@@ -113,6 +114,9 @@ class Quantizer:
     def c_struct(self) -> L.TqQuantizer:
         return self._c
 
+    def c_ref(self):
+        return ctypes.byref(self._c)
+
 
 @dataclass
 class PackedCache:
@@ -140,6 +144,9 @@ class PackedCache:
         v = L.TqCacheView(key[0], key[1], key[2], key[3], sb, sh, sn)
         self.__dict__["_view"] = (key, v)
         return v
+
+    def c_ref(self):
+        return ctypes.byref(self.view())
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in (self.codes, self.qjl, self.norms, self.rnorms)
@@ -352,25 +359,44 @@ def search_topk(qz: Quantizer, queries: torch.Tensor, db: PackedCache, k: int):
 
 # ------------------------------------------------------------ paged cache
 
-def _on(t: torch.Tensor, stream=None):
-    """(device guard, stream handle) of a call whose tensors live with t."""
-    s = stream if stream is not None else torch.cuda.current_stream(t.device)
-    return torch.cuda.device(t.device), s.cuda_stream
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _on(device: int, stream=None):
+    """(guard, stream handle) of a call on tensors of this device."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    guard = _NO_GUARD if torch.cuda.current_device() == device else torch.cuda.device(device)
+    return guard, stream.cuda_stream
 
 
 def _strides(t: Optional[torch.Tensor]):
     """Element strides over the first two dims (0 where the extent is 1)."""
-    return (0, 0) if t is None else tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1))
+    if t is None:
+        return 0, 0
+    (n, m, _), (a, b, c) = t.shape, t.stride()
+    assert c == 1, "the last dim must be contiguous"
+    return (a if n > 1 else 0), (b if m > 1 else 0)
 
 
-def _same_device(t: torch.Tensor, **others) -> None:
-    for name, o in others.items():
-        assert o is None or o.device == t.device, f"{name} is on {o.device}, not on {t.device}"
-
-
-def _check_i32(**ts) -> None:
+def _check(device: int, dtype, **ts) -> None:
+    """Contiguous tensors of one type on this device (None: not given)."""
     for name, t in ts.items():
-        assert t is None or (t.dtype == torch.int32 and t.is_contiguous()), f"{name}: a contiguous int32 tensor"
+        if t is not None and not (t.dtype is dtype and t.get_device() == device and t.is_contiguous()):
+            raise AssertionError(f"{name}: a contiguous {dtype} tensor on device {device}, got {t.dtype} on {t.device}")
+
+
+def _check_caches(device: int, kq: Quantizer, vq: Quantizer, kcache, vcache) -> None:
+    for t in (kcache.norms, vcache.norms, kq.signs, vq.signs):
+        assert t.get_device() == device, f"caches and quantizers must be on device {device}"
+
+
+def _check_table(device: int, table: torch.Tensor, R: int):
+    """(row stride, entries a row) of a block table [R, max_pages]."""
+    (n, width), (stride, one) = table.shape, table.stride()
+    assert n == R and table.dtype is torch.int32 and table.get_device() == device and (one == 1 or width <= 1), \
+        "block_table: an int32 tensor [R, max_pages] on the call's device"
+    return (stride if R > 1 else width), width
 
 
 @dataclass
@@ -395,6 +421,9 @@ class PagePlanner:
         self.plan = PagePlan(torch.empty(max_tokens, dtype=torch.int64, device=device), torch.empty(max_tokens, **i32),
                              torch.empty(n_requests + 1, **i32), torch.empty(n_requests, **i32),
                              torch.empty(n_requests, **i32), torch.empty(1, **i32))
+        p = self.plan
+        self.device = p.slots.get_device()
+        self._out = tuple(t.data_ptr() for t in (p.slots, p.positions, p.cu_new, p.seq_lens, p.status, p.n_free))
 
     def __call__(self, lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, n_free: torch.Tensor,
                  block_table: torch.Tensor, stream=None) -> PagePlan:
@@ -403,19 +432,15 @@ class PagePlanner:
         (n_free: a one-element int32 device tensor) and are entered in
         block_table [R, max_pages] (int32, in place).  Pass plan.seq_lens and
         plan.n_free on by copying them: they may not be this call's inputs."""
-        p = self.plan
-        assert lens.shape == (self.R,) and new_lens.shape == (self.R,) and n_free.numel() == 1
-        assert block_table.dim() == 2 and block_table.shape[0] == self.R and free_pages.dim() == 1
-        assert block_table.dtype == torch.int32 and (block_table.shape[1] <= 1 or block_table.stride(1) == 1)
-        _check_i32(lens=lens, new_lens=new_lens, free_pages=free_pages, n_free=n_free)
-        _same_device(p.slots, lens=lens, new_lens=new_lens, free_pages=free_pages, n_free=n_free,
-                     block_table=block_table)
-        guard, s = _on(lens, stream)
+        p, R = self.plan, self.R
+        assert lens.shape == (R,) and new_lens.shape == (R,) and n_free.numel() == 1 and free_pages.dim() == 1
+        _check(self.device, torch.int32, lens=lens, new_lens=new_lens, free_pages=free_pages, n_free=n_free)
+        stride, width = _check_table(self.device, block_table, R)
+        guard, s = _on(self.device, stream)
         with guard:
             L.check(L.lib().tq_page_plan(
-                self.R, self.page_size, _ptr(lens), _ptr(new_lens), _ptr(free_pages), free_pages.numel(), _ptr(n_free),
-                _ptr(block_table), max(block_table.stride(0), 0), block_table.shape[1], self.max_tokens, _ptr(p.slots),
-                _ptr(p.positions), _ptr(p.cu_new), _ptr(p.seq_lens), _ptr(p.status), _ptr(p.n_free), s))
+                R, self.page_size, lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_pages.shape[0],
+                n_free.data_ptr(), block_table.data_ptr(), stride, width, self.max_tokens, *self._out, s))
         return p
 
 
@@ -446,8 +471,10 @@ class Rope:
         self._c = L.TqRope(2 * n, L.TQ_ROPE_ADJACENT if pairing == "adjacent" else L.TQ_ROPE_HALF, self.n_axes,
                            _ptr(self.inv_freq), _ptr(self.axis))
 
-    def c_struct(self) -> L.TqRope:
-        return self._c
+        self._ref = ctypes.byref(self._c)
+
+    def c_ref(self):
+        return self._ref
 
 
 def paged_append(kq: Quantizer, vq: Quantizer, k: torch.Tensor, v: torch.Tensor, kcache: PackedCache,
@@ -460,37 +487,37 @@ def paged_append(kq: Quantizer, vq: Quantizer, k: torch.Tensor, v: torch.Tensor,
     are turned to positions ([T] or [n_axes, T], int32) first, and the turned
     q is returned (q_out, or a new tensor)."""
     T, Hkv, d = k.shape
-    assert d == kq.d and v.shape == k.shape and v.dtype == k.dtype and k.dtype in _DTYPES
-    assert k.stride(2) == 1 and v.stride(2) == 1
-    assert slots.shape == (T,) and slots.dtype == torch.int64 and slots.is_contiguous()
-    n_pages, H, P = kcache.shape
-    assert H == Hkv and vcache.shape == kcache.shape
-    pos_stride = 0
+    dev, dt = k.get_device(), k.dtype
+    assert d == kq.d and v.shape == k.shape and v.dtype is dt and dt in _DTYPES
+    assert v.get_device() == dev and slots.shape == (T,)
+    _check(dev, torch.int64, slots=slots)
+    n_pages, H, P = kcache.norms.shape
+    assert H == Hkv and vcache.norms.shape == kcache.norms.shape
+    _check_caches(dev, kq, vq, kcache, vcache)
+    pos_stride, rp, pp = 0, None, None
     if rope is not None:
-        assert positions is not None and positions.dtype == torch.int32
+        assert positions is not None and positions.dtype is torch.int32 and positions.get_device() == dev
         assert positions.shape == (rope.n_axes, T) or (rope.n_axes == 1 and positions.shape == (T,))
         assert T <= 1 or positions.stride(-1) == 1
+        assert rope.inv_freq.get_device() == dev
         pos_stride = positions.stride(0) if rope.n_axes > 1 else 0
+        rp, pp = rope.c_ref(), positions.data_ptr()
     else:
         assert q is None and positions is None, "query rows and positions need a rope"
     Hq = 0
     if q is not None:
         Hq = q.shape[1]
-        assert q.shape == (T, Hq, d) and q.dtype == k.dtype and q.stride(2) == 1
+        assert q.shape == (T, Hq, d) and q.dtype is dt and q.get_device() == dev
         if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
-        assert q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.is_contiguous()
-    _same_device(k, v=v, q=q, q_out=q_out, slots=slots, positions=positions, kcache=kcache.norms,
-                 vcache=vcache.norms, kq=kq.centroids, vq=vq.centroids,
-                 rope=None if rope is None else rope.inv_freq)
-    kv, vv = kcache.view(), vcache.view()
-    guard, s = _on(k, stream)
+            q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+        assert q_out.shape == q.shape
+        _check(dev, dt, q_out=q_out)
+    guard, s = _on(dev, stream)
     with guard:
         L.check(L.lib().tq_paged_append(
-            ctypes.byref(kq.c_struct()), ctypes.byref(vq.c_struct()),
-            None if rope is None else ctypes.byref(rope.c_struct()), _ptr(positions), pos_stride, _DTYPES[k.dtype], T,
-            Hq, Hkv, _ptr(q), *_strides(q), _ptr(k), *_strides(k), _ptr(v), *_strides(v),
-            _ptr(q_out) if q is not None else None, ctypes.byref(kv), ctypes.byref(vv), n_pages, P, _ptr(slots), s))
+            kq.c_ref(), vq.c_ref(), rp, pp, pos_stride, _DTYPES[dt], T, Hq, Hkv, _ptr(q), *_strides(q), k.data_ptr(),
+            *_strides(k), v.data_ptr(), *_strides(v), _ptr(q_out) if Hq else None, kcache.c_ref(), vcache.c_ref(),
+            n_pages, P, slots.data_ptr(), s))
     return q_out if q is not None else None
 
 
@@ -498,18 +525,18 @@ def paged_dequant(qz: Quantizer, cache: PackedCache, slots: torch.Tensor, dtype=
                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """tq_paged_dequant: the vectors of the records at slots [T] (int64; -1
     gives zeros) as [T, H, d] in dtype."""
-    n_pages, H, P = cache.shape
-    assert slots.dim() == 1 and slots.dtype == torch.int64 and slots.is_contiguous()
-    T = slots.shape[0]
+    n_pages, H, P = cache.norms.shape
+    (T,), dev = slots.shape, cache.norms.get_device()
+    _check(dev, torch.int64, slots=slots)
+    _check_caches(dev, qz, qz, cache, cache)
     if out is None:
         out = torch.empty((T, H, qz.d), dtype=dtype, device=cache.norms.device)
-    assert out.shape == (T, H, qz.d) and out.dtype in _DTYPES and out.is_contiguous()
-    _same_device(out, slots=slots, cache=cache.norms, qz=qz.centroids)
-    v = cache.view()
-    guard, s = _on(out, stream)
+    assert out.shape == (T, H, qz.d) and out.dtype in _DTYPES
+    _check(dev, out.dtype, out=out)
+    guard, s = _on(dev, stream)
     with guard:
-        L.check(L.lib().tq_paged_dequant(ctypes.byref(qz.c_struct()), ctypes.byref(v), n_pages, P, T, H, _ptr(slots),
-                                         _DTYPES[out.dtype], _ptr(out), s))
+        L.check(L.lib().tq_paged_dequant(qz.c_ref(), cache.c_ref(), n_pages, P, T, H, slots.data_ptr(),
+                                         _DTYPES[out.dtype], out.data_ptr(), s))
     return out
 
 
@@ -525,7 +552,7 @@ class PagedAttention:
         with torch.cuda.device(torch.device(device)):
             nb = int(L.lib().tq_paged_attention_workspace_bytes(max_requests, max_tokens, Hq, Hkv, kq.d))
         self.workspace = torch.empty(max(nb, 16), dtype=torch.uint8, device=device)
-        self.ws_bytes = nb
+        self.device, self._ws, self.ws_bytes = self.workspace.get_device(), self.workspace.data_ptr(), nb
 
     def __call__(self, q: torch.Tensor, kcache: PackedCache, vcache: PackedCache, block_table: torch.Tensor,
                  kv_lens: torch.Tensor, cu_q: Optional[torch.Tensor] = None, max_q: Optional[int] = None,
@@ -538,34 +565,33 @@ class PagedAttention:
         rows' included).  max_q: an upper bound of the row counts (default:
         1 without cu_q, else T).  Returns out [T, Hq, d] in q's dtype; lse
         [T, Hq] (fp32), if given, gets the logarithm of the softmax's sums."""
-        T, Hq, d = q.shape
-        R = kv_lens.shape[0]
-        n_pages, Hkv, P = kcache.shape
-        assert (Hq, Hkv, d) == (self.Hq, self.Hkv, self.kq.d) and q.dtype in _DTYPES and q.stride(2) == 1
-        assert vcache.shape == kcache.shape
+        (T, Hq, d), (R,), dt, dev = q.shape, kv_lens.shape, q.dtype, self.device
+        n_pages, Hkv, P = kcache.norms.shape
+        assert (Hq, Hkv, d) == (self.Hq, self.Hkv, self.kq.d) and vcache.norms.shape == kcache.norms.shape
+        assert dt in _DTYPES and q.get_device() == dev
         assert R <= self.max_requests and T <= self.max_tokens, "more requests or rows than the workspace is for"
-        assert block_table.dim() == 2 and block_table.shape[0] == R and block_table.dtype == torch.int32
-        assert block_table.shape[1] <= 1 or block_table.stride(1) == 1
         assert cu_q is None or cu_q.shape == (R + 1,)
-        _check_i32(kv_lens=kv_lens, cu_q=cu_q)
+        _check(dev, torch.int32, kv_lens=kv_lens, cu_q=cu_q)
+        _check_caches(dev, self.kq, self.vq, kcache, vcache)
+        stride, width = _check_table(dev, block_table, R)
         if max_q is None:
             max_q = 1 if cu_q is None else max(T, 1)
         if scale is None:
             scale = 1.0 / math.sqrt(d)
         if out is None:
-            out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
-        assert out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()
-        assert lse is None or (lse.shape == (T, Hq) and lse.dtype == torch.float32 and lse.is_contiguous())
-        _same_device(q, kcache=kcache.norms, vcache=vcache.norms, block_table=block_table, kv_lens=kv_lens, cu_q=cu_q,
-                     out=out, lse=lse, workspace=self.workspace, kq=self.kq.centroids, vq=self.vq.centroids)
-        kv, vv = kcache.view(), vcache.view()
-        guard, s = _on(q, stream)
+            out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+        else:
+            assert out.shape == q.shape
+            _check(dev, dt, out=out)
+        if lse is not None:
+            assert lse.shape == (T, Hq)
+            _check(dev, torch.float32, lse=lse)
+        guard, s = _on(dev, stream)
         with guard:
             L.check(L.lib().tq_paged_attention(
-                ctypes.byref(self.kq.c_struct()), ctypes.byref(self.vq.c_struct()), _ptr(q), _DTYPES[q.dtype], T, Hq,
-                Hkv, *_strides(q), ctypes.byref(kv), ctypes.byref(vv), n_pages, P, _ptr(block_table),
-                max(block_table.stride(0), 0), R, block_table.shape[1], _ptr(kv_lens), _ptr(cu_q), max_q, float(scale),
-                int(causal), int(window), _ptr(out), _ptr(lse), _ptr(self.workspace), self.ws_bytes, s))
+                self.kq.c_ref(), self.vq.c_ref(), q.data_ptr(), _DTYPES[dt], T, Hq, Hkv, *_strides(q), kcache.c_ref(),
+                vcache.c_ref(), n_pages, P, block_table.data_ptr(), stride, R, width, kv_lens.data_ptr(), _ptr(cu_q),
+                max_q, scale, int(causal), window, out.data_ptr(), _ptr(lse), self._ws, self.ws_bytes, s))
         return out
 
 

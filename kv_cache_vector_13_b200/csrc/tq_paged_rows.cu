@@ -40,12 +40,21 @@ constexpr int kStep = 16;                // tokens per step
 constexpr uint32_t kTabAddr = 0x10000u;  // the pair tables: 64 KiB at this shared address
 constexpr uint32_t kPartAddr = 0x20000u; // the warps' partial sums
 constexpr int kMaxRows = 8;
+constexpr int kStages = 3;               // a warp's steps in shared memory
 
 template <int D>
 struct Cfg {
-  static constexpr int kWarps = 16;
+#ifndef RW
+#define RW 16
+#endif
+  static constexpr int kWarps = RW;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kPitch = D + 4;  // floats of a partial row (no bank clash between rows)
+  // a step: K codes, V codes, 16 norms of each
+  static constexpr int kStepBytes = kStep * D + 2 * kStep * 4;
+  static constexpr int kRing = kStages * kStepBytes;
+  // rings above the tables (the partial sums reuse the space), the rest below
+  static constexpr int kHigh = (227 * 1024 - (int)kPartAddr) / kRing < kWarps ? (227 * 1024 - (int)kPartAddr) / kRing : kWarps;
 };
 
 // Shared memory below the tables.
@@ -57,11 +66,13 @@ struct Low {
   float f[kMaxRows];               // logit factor of each row
   float m[Cfg<D>::kWarps][kMaxRows], l[Cfg<D>::kWarps][kMaxRows];
   float scale[2];                  // the tables' scales
+  float e[kMaxRows][Cfg<D>::kWarps], top[kMaxRows], sum[kMaxRows];  // merge of the warps
 };
 
 template <int D>
 __host__ __device__ constexpr uint32_t smem_end() {
-  return kPartAddr + Cfg<D>::kWarps * kMaxRows * Cfg<D>::kPitch * 4;
+  constexpr uint32_t parts = Cfg<D>::kWarps * kMaxRows * Cfg<D>::kPitch * 4, rings = Cfg<D>::kHigh * Cfg<D>::kRing;
+  return kPartAddr + (parts > rings ? parts : rings);
 }
 
 struct RowsParams {
@@ -108,7 +119,9 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 // Table read of byte k of w: shared address {lane, byte k, table}.
 template <int K>
 __device__ __forceinline__ uint32_t pair(uint32_t w, uint32_t base) {
-  return lds32(__byte_perm(w, base, 0x7604 | (K << 4)));
+  uint32_t a;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(a) : "r"(w), "r"(base), "n"(0x7604 | (K << 4)));
+  return lds32(a);
 }
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -126,29 +139,45 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// Codes and norms of one step as a lane needs them.
+// Coordinate g (D/8) + 2 j + b of an unfinished row is kept at place 16 j + 2 g + b.
 template <int D>
-struct Codes {
-  uint32_t k[2][D / 32];  // tokens g and 8 + g, coordinates [q D/4, (q + 1) D/4)
-  uint32_t v[4][D / 64];  // tokens 2q, 2q+1, 8+2q, 9+2q, coordinates [g D/8, (g + 1) D/8)
-  float kn[2], vn[2];     // tokens g and 8 + g
-};
+__device__ __forceinline__ int place(int k) {
+  const int u = k % (D / 8);
+  return 16 * (u / 2) + 2 * (k / (D / 8)) + (u & 1);
+}
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 template <int N>
-__device__ __forceinline__ void ldg_words(const uint8_t *p, uint32_t (&w)[N]) {
-  if constexpr (N == 4) {
-    const uint4 t = __ldg(reinterpret_cast<const uint4 *>(p));
-    w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
-  } else if constexpr (N == 2) {
-    const uint2 t = __ldg(reinterpret_cast<const uint2 *>(p));
-    w[0] = t.x; w[1] = t.y;
-  } else {
-    w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
-  }
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(a));
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+
+// Where the staged V codes of token t, 16-byte word c, lie: two tokens swap
+// places in every other group of four, and word pairs in every other pair of
+// tokens, so that a half-warp's reads (8 bytes of tokens 0, 2, 4, 6) fall into
+// different banks.
+template <int D>
+__device__ __forceinline__ uint32_t v_place(int t, int c) {
+  return (uint32_t)((t ^ ((t >> 2) & 1)) * (D / 2) + (D == 128 ? (c ^ (((t >> 1) & 1) << 1)) * 16 : c * 16));
 }
 
 // P4: up to 4 query rows a tile, hi and lo in one product; else up to 8.
-// UNIT: the tokens of a page lie side by side.
+// UNIT: the tokens of a page lie side by side, and K and V records alike.
 template <int D, bool P4, bool UNIT>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr int W = Cfg<D>::kWarps, NT = Cfg<D>::kThreads, PITCH = Cfg<D>::kPitch;
@@ -173,7 +202,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
   const uint32_t dyn = (uint32_t)__cvta_generic_to_shared(s_raw);
   uint32_t dyn_bytes;
   asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn_bytes));
-  if (dyn + sizeof(Low<D>) > kTabAddr || dyn + dyn_bytes < smem_end<D>()) {
+  if (dyn + sizeof(Low<D>) + (W - Cfg<D>::kHigh) * Cfg<D>::kRing > kTabAddr || dyn + dyn_bytes < smem_end<D>()) {
     if (tid == 0) {
       atomicOr(p.faults, kFaultSmemLayout);
       p.desc[c] = make_int4(0, 0, 0, 0);
@@ -251,9 +280,20 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
       r_base += w;
     }
   }
-  const uint32_t ktab = kTabAddr + 4 * lane, vtab = ktab + 128;
+  uint32_t ktab, vtab;  // opaque, so that a table address stays one byte permute
+  asm("mov.b32 %0, %1;" : "=r"(ktab) : "r"(kTabAddr + 4 * lane));
+  asm("mov.b32 %0, %1;" : "=r"(vtab) : "r"(kTabAddr + 4 * lane + 128));
   const float kscale = a.scale * 1.4426950408889634f / (a.kq.sqrt_d * s_scale[0]);
   const float vscale = 1.0f / (a.vq.sqrt_d * s_scale[1]);
+
+  // the lane's 16 bytes of a step's records (of the first 8 tokens for d = 128), and where they go
+  const uint8_t *kc_lane = a.k.codes + 16 * lane, *vc_lane = a.v.codes + 16 * lane;
+  const uint32_t v_to = v_place<D>(lane / (D / 32), lane % (D / 32));
+  // and the lane's reads: V of tokens 2 q4 and 2 q4 + 1
+  const uint32_t v_at0 = v_place<D>(2 * q4, g * (D / 16) / 16) + (g * (D / 16)) % 16;
+  const uint32_t v_at1 = v_place<D>(2 * q4 + 1, g * (D / 16) / 16) + (g * (D / 16)) % 16;
+  const uint32_t ring = warp < Cfg<D>::kHigh ? kPartAddr + warp * Cfg<D>::kRing
+                                             : kTabAddr - (warp - Cfg<D>::kHigh + 1) * Cfg<D>::kRing;
 
   while (at < end && r < a.R) {
     // ---- the piece: steps [s0, s1) of unit (r, h, tile)
@@ -265,6 +305,55 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
     const int h = unit / req.tiles, tile = unit - h * req.tiles;
     const int row0 = tile * RT;
     const int nrows = min(RT, req.n * G - row0);
+
+    const int32_t *row = a.table + (int64_t)r * a.table_stride;
+    const int n_steps = s1 - s0 > warp ? (s1 - s0 - warp + W - 1) / W : 0;
+    // The records of 8 of the warp's steps, step it + lane % 8 a lane, found a batch ahead; -1 without a page
+    // and behind the piece's last step.
+    int64_t krec, vrec, krec2, vrec2;
+    auto find = [&](int it, int64_t &kr, int64_t &vr) {
+      const int s = s0 + warp + (it + (lane & 7)) * W;
+      kr = vr = -1;
+      const int t0 = s * kStep;
+      if (s < s1 && t0 < req.kv) {
+        const int page = t0 / a.page_size, off = t0 - page * a.page_size;
+        const int id = __ldg(row + page);
+        if ((unsigned)id < (unsigned)a.n_pages) {
+          kr = id * a.k.sb + h * a.k.sh + off * a.k.sn;
+          vr = UNIT ? kr : id * a.v.sb + h * a.v.sh + off * a.v.sn;
+        } else {
+          atomicOr(p.faults, kFaultIndex);
+        }
+      }
+    };
+    // Step it's records into its stage, asynchronously; bit it % 3 of `ok` says whether there are any.
+    uint32_t ok = 0;
+    auto issue = [&](int it, int stage) {
+      const int64_t kr = __shfl_sync(dev::kFull, krec, it & 7);
+      const int64_t vr = UNIT ? kr : __shfl_sync(dev::kFull, vrec, it & 7);
+      const uint32_t to = ring + stage * Cfg<D>::kStepBytes;
+      ok = (ok & ~(1u << stage)) | ((kr >= 0 ? 1u : 0u) << stage);
+      if (kr >= 0) {
+        constexpr int CH = D / 32;  // 16-byte words of a record
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i) {
+          const int t = (lane + 32 * i) / CH;
+          const int64_t o = UNIT ? (int64_t)0 : t * (a.k.sn - 1) * (D / 2), u = UNIT ? (int64_t)0 : t * (a.v.sn - 1) * (D / 2);
+          cp_async16(to + 16 * (lane + 32 * i), kc_lane + kr * (D / 2) + o + 512 * i);
+          cp_async16(to + kStep * (D / 2) + v_to + 512 * i, vc_lane + vr * (D / 2) + u + 512 * i);
+        }
+        const int t = lane & 15;
+        cp_async4(to + kStep * D + 4 * lane,
+                  lane < 16 ? a.k.norms + kr + (UNIT ? t : t * a.k.sn) : a.v.norms + vr + (UNIT ? t : t * a.v.sn));
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (n_steps > 0) {
+      find(0, krec, vrec);
+      find(8, krec2, vrec2);
+      issue(0, 0);
+      issue(1, 1);
+    }
 
     // ---- query rows: sign flips, FWHT, a power of two that brings the largest into [1, 2)
     for (int i = warp; i < RT; i += W) {
@@ -326,86 +415,21 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 
-    const int32_t *row = a.table + (int64_t)r * a.table_stride;
-    const int n_steps = s1 - s0 > warp ? (s1 - s0 - warp + W - 1) / W : 0;
-    // The records of 8 of the warp's steps, step it + lane % 8 a lane; -1 without a page.  They are found a
-    // batch ahead and brought into L2 (lane / 8: codes and norms of K and of V).
-    int64_t krec, vrec, krec2, vrec2;
-    auto find = [&](int it, int64_t &kr, int64_t &vr) {
-      const int s = s0 + warp + (it + (lane & 7)) * W;
-      kr = vr = -1;
-      const int t0 = s * kStep;
-      if (s < s1 && t0 < req.kv) {
-        const int page = t0 / a.page_size, off = t0 - page * a.page_size;
-        const int id = __ldg(row + page);
-        if ((unsigned)id < (unsigned)a.n_pages) {
-          kr = id * a.k.sb + h * a.k.sh + off * a.k.sn;
-          vr = id * a.v.sb + h * a.v.sh + off * a.v.sn;
-        } else {
-          atomicOr(p.faults, kFaultIndex);
-        }
-      }
-    };
-    auto warm = [&](int64_t kr, int64_t vr) {
-      if (!UNIT || kr < 0) return;
-      const int what = lane >> 3;
-      const bool norm = what & 1;
-      const char *at = norm ? reinterpret_cast<const char *>((what & 2 ? a.v.norms : a.k.norms) + (what & 2 ? vr : kr))
-                            : reinterpret_cast<const char *>((what & 2 ? a.v.codes : a.k.codes) + (what & 2 ? vr : kr) * (D / 2));
-      // a run of norms may begin inside a 16-byte word: the words that hold it
-      const uintptr_t lo = (uintptr_t)at & ~(uintptr_t)15;
-      const uint32_t n = norm ? (uint32_t)(((uintptr_t)at + 4 * kStep + 15 - lo) & ~(uintptr_t)15) : kStep * (D / 2);
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(lo), "r"(n) : "memory");
-    };
-    auto load_k = [&](int64_t kr, Codes<D> &cd) {
-      if constexpr (UNIT) {
-        const uint8_t *c = a.k.codes + kr * (D / 2) + (g * (D / 2) + q4 * (D / 8));
-        ldg_words(c, cd.k[0]);
-        ldg_words(c + 8 * (D / 2), cd.k[1]);
-        const float *n = a.k.norms + kr + g;
-        cd.kn[0] = __ldg(n);
-        cd.kn[1] = __ldg(n + 8);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          ldg_words(a.k.codes + (kr + (8 * i + g) * a.k.sn) * (D / 2) + q4 * (D / 8), cd.k[i]);
-          cd.kn[i] = __ldg(a.k.norms + kr + (8 * i + g) * a.k.sn);
-        }
-      }
-    };
-    auto load_v = [&](int64_t vr, Codes<D> &cd) {
-      if constexpr (UNIT) {
-        const uint8_t *c = a.v.codes + vr * (D / 2) + (q4 * D + g * (D / 16));
-        ldg_words(c, cd.v[0]);
-        ldg_words(c + D / 2, cd.v[1]);
-        ldg_words(c + 8 * (D / 2), cd.v[2]);
-        ldg_words(c + 9 * (D / 2), cd.v[3]);
-        const float *n = a.v.norms + vr + g;
-        cd.vn[0] = __ldg(n);
-        cd.vn[1] = __ldg(n + 8);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          ldg_words(a.v.codes + (vr + (8 * (i >> 1) + 2 * q4 + (i & 1)) * a.v.sn) * (D / 2) + g * (D / 16), cd.v[i]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) cd.vn[i] = __ldg(a.v.norms + vr + (8 * i + g) * a.v.sn);
-      }
-    };
     // The running softmax of the lane's rows over its tokens g and 8 + g (value 2 i + o: token 8 i + g, row o):
     // scores in, weights times value norms out.  M is a reference that moves only when one of them would pass 2^8.
-    auto soft = [&](auto edge, int t0, float (&t)[4], const Codes<D> &cd) {
+    auto soft = [&](auto edge, int t0, float (&t)[4], const float (&kn)[2], const float (&vn)[2]) {
       constexpr bool EDGE = decltype(edge)::value;
       float lv[2], mx[2], s[4];
       bool seen[4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int j = t0 + 8 * i + g;
-        lv[i] = fmaxf(log2_approx(cd.vn[i]), -64.f);
+        lv[i] = fmaxf(log2_approx(vn[i]), -64.f);
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
           const int e = 2 * i + o;
           seen[e] = !EDGE || (j >= see_lo[o] && j < see_hi[o] && j < req.kv);
-          s[e] = t[e] * (f[o] * cd.kn[i]);
+          s[e] = t[e] * (f[o] * kn[i]);
           t[e] = s[e] - M[o];
           if (EDGE && !seen[e]) t[e] = -INFINITY;
         }
@@ -433,42 +457,33 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
       for (int e = 0; e < 4; ++e) {
         t[e] = exp2_approx(t[e]);
         l[e & 1] += t[e];
-        t[e] *= cd.vn[e >> 1];
+        t[e] *= vn[e >> 1];
         if (EDGE && !seen[e]) t[e] = 0.f;
       }
     };
 
-    Codes<D> cd;
-    bool have = false;  // the step has a page
-    if (n_steps > 0) {
-      find(0, krec, vrec);
-      warm(krec, vrec);
-      find(8, krec2, vrec2);
-      const int64_t kr = __shfl_sync(dev::kFull, krec, 0), vr = __shfl_sync(dev::kFull, vrec, 0);
-      have = kr >= 0;
-      if (have) {
-        load_k(kr, cd);
-        load_v(vr, cd);
-      }
-    }
+    int stage = 0;
     for (int it = 0; it < n_steps; ++it) {
       const int t0 = (s0 + warp + it * W) * kStep;
-      if ((it & 7) == 3) warm(krec2, vrec2);
-      if ((it & 7) == 7) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
+      if (((it + 2) & 7) == 0) {
         krec = krec2;
         vrec = vrec2;
-        find(it + 9, krec2, vrec2);
+        find(it + 10, krec2, vrec2);
       }
-      // find() gives -1 behind the piece's last step
-      if (!have) {
-        const int64_t kr = __shfl_sync(dev::kFull, krec, (it + 1) & 7);
-        const int64_t vr = __shfl_sync(dev::kFull, vrec, (it + 1) & 7);
-        have = kr >= 0;
-        if (have) {
-          load_k(kr, cd);
-          load_v(vr, cd);
-        }
-        continue;
+      const int at_stage = stage;
+      issue(it + 2, stage == 0 ? 2 : stage - 1);  // the stage of step it - 1
+      stage = stage == 2 ? 0 : stage + 1;
+      if (!(ok >> at_stage & 1)) continue;
+      const uint32_t from = ring + at_stage * Cfg<D>::kStepBytes;
+      uint32_t ck[2][D / 32], cv[4][D / 64];  // K of tokens g, 8 + g; V of 2 q4, 2 q4 + 1, 8 + 2 q4, 9 + 2 q4
+      float kn[2], vn[2];                     // of tokens g, 8 + g
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        lds_words(from + (8 * i + g) * (D / 2) + q4 * (D / 8), ck[i]);
+        kn[i] = lds_f32(from + kStep * D + 4 * (8 * i + g));
+        vn[i] = lds_f32(from + kStep * D + 64 + 4 * (8 * i + g));
       }
       // ---- scores: value 2 i + o is token 8 i + g, column 2 q4 + o
       float sc[2][4];
@@ -478,7 +493,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
         for (int e = 0; e < 4; ++e) sc[c2][e] = 0.f;
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
-        const uint32_t x = cd.k[0][w], y = cd.k[1][w];
+        const uint32_t x = ck[0][w], y = ck[1][w];
         const uint32_t a0 = pair<0>(x, ktab), a1 = pair<0>(y, ktab), a2 = pair<1>(x, ktab), a3 = pair<1>(y, ktab);
         const uint32_t b0 = pair<2>(x, ktab), b1 = pair<2>(y, ktab), b2 = pair<3>(x, ktab), b3 = pair<3>(y, ktab);
 #pragma unroll
@@ -495,9 +510,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
         if (P4) t[e] += __shfl_xor_sync(dev::kFull, t[e], 2);  // the hi and lo columns
       }
       if (t0 + kStep > full_hi || t0 < full_lo)
-        soft(std::true_type{}, t0, t, cd);
+        soft(std::true_type{}, t0, t, kn, vn);
       else
-        soft(std::false_type{}, t0, t, cd);
+        soft(std::false_type{}, t0, t, kn, vn);
       // weights to operand words: fp16 pairs of two rows at a token, transposed to two tokens of a row
       uint32_t pb[QS][2];
 #pragma unroll
@@ -513,15 +528,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
           pb[QS - 1][i] = transpose8(wl);
         }
       }
-      {
-        const int64_t kr = __shfl_sync(dev::kFull, krec, (it + 1) & 7);
-        have = kr >= 0;
-        if (have) load_k(kr, cd);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        lds_words(from + kStep * (D / 2) + v_at0 + 8 * i * (D / 2), cv[2 * i]);
+        lds_words(from + kStep * (D / 2) + v_at1 + 8 * i * (D / 2), cv[2 * i + 1]);
       }
       // ---- values: tokens 2 q4 and 2 q4 + 1 interleaved (even and odd coordinates apart)
 #pragma unroll
       for (int w = 0; w < D / 64; ++w) {
-        const uint32_t x0 = cd.v[0][w], x1 = cd.v[1][w], x2 = cd.v[2][w], x3 = cd.v[3][w];
+        const uint32_t x0 = cv[0][w], x1 = cv[1][w], x2 = cv[2][w], x3 = cv[3][w];
         const uint32_t e0 = (x0 & 0x0f0f0f0fu) | ((x1 << 4) & 0xf0f0f0f0u);
         const uint32_t o0 = ((x0 >> 4) & 0x0f0f0f0fu) | (x1 & 0xf0f0f0f0u);
         const uint32_t e1 = (x2 & 0x0f0f0f0fu) | ((x3 << 4) & 0xf0f0f0f0u);
@@ -537,11 +552,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
         tile(std::integral_constant<int, 2>{});
         tile(std::integral_constant<int, 3>{});
       }
-      const int64_t vr = __shfl_sync(dev::kFull, vrec, (it + 1) & 7);
-      if (have) load_v(vr, cd);
     }
+    // all copies of this warp are in, and every warp is through with its ring before the sums go there
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
 
-    // ---- the warps' sums: coordinate g (D/8) + 2 j + b of a row at 16 j + 2 g + b
+    // ---- the warps' sums
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
       float t = l[o];
@@ -567,35 +583,45 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
       }
     __syncthreads();
     const bool starts = s0 == req.lo, ends = s1 == req.hi;
-    for (int i = warp; i < nrows; i += W) {
+    // each warp's factor for each row
+    if (tid < W * RT) {
+      const int w = tid / RT, i = tid % RT;
       float m = s_m[0][i];
 #pragma unroll
-      for (int w = 1; w < W; ++w) m = fmaxf(m, s_m[w][i]);
-      float L = 0.f, y[D / 32];
+      for (int x = 1; x < W; ++x) m = fmaxf(m, s_m[x][i]);
+      sm.e[i][w] = exp2f(s_m[w][i] - m);
+      if (w == 0) sm.top[i] = m;
+    }
+    __syncthreads();
+    float *slot = p.slots + (size_t)(2 * c + (starts ? 1 : 0)) * kMaxRows * (D + 2);
+    for (int u = tid; u < nrows * D; u += NT) {
+      const int i = u / D, k = u % D;  // place k of the row
+      float y = 0.f;
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) y[e] = 0.f;
+      for (int w = 0; w < W; ++w) y = fmaf(sm.e[i][w], parts[(w * kMaxRows + i) * PITCH + k], y);
+      if (starts && ends)
+        parts[i * PITCH + k] = y;  // only this thread has read it
+      else
+        slot[i * (D + 2) + k] = y;
+    }
+    if (tid < nrows) {
+      float L = 0.f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float s = exp2f(s_m[w][i] - m);
-        L += s * s_l[w][i];
-        const float *src = parts + ((size_t)w * kMaxRows + i) * PITCH;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-          const int k = lane * (D / 32) + e, u = k % (D / 8);
-          y[e] = fmaf(s, src[16 * (u / 2) + 2 * (k / (D / 8)) + (u & 1)], y[e]);
-        }
+      for (int w = 0; w < W; ++w) L = fmaf(sm.e[tid][w], s_l[w][tid], L);
+      sm.sum[tid] = L;
+      if (!(starts && ends)) {
+        slot[tid * (D + 2) + D] = sm.top[tid];
+        slot[tid * (D + 2) + D + 1] = L;
       }
-      if (starts && ends) {
-        const int qi = (row0 + i) / G;
-        store_out<D>(a, (int64_t)req.q0 + qi, h * G + (row0 + i) - qi * G, lane, y, m, L, vscale);
-      } else {
-        float *slot = p.slots + ((size_t)(2 * c + (starts ? 1 : 0)) * kMaxRows + i) * (D + 2);
+    }
+    if (starts && ends) {
+      __syncthreads();
+      for (int i = warp; i < nrows; i += W) {
+        float y[D / 32];
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) slot[lane * (D / 32) + e] = y[e];
-        if (lane == 0) {
-          slot[D] = m;
-          slot[D + 1] = L;
-        }
+        for (int e = 0; e < D / 32; ++e) y[e] = parts[i * PITCH + place<D>(lane * (D / 32) + e)];
+        const int qi = (row0 + i) / G;
+        store_out<D>(a, (int64_t)req.q0 + qi, h * G + (row0 + i) - qi * G, lane, y, sm.top[i], sm.sum[i], vscale);
       }
     }
     if (starts && !ends) {
@@ -620,41 +646,68 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
 }
 
 // Merges the pieces of the unit that starts last in CTA c's range and goes on
-// behind it, a warp a row, in the order of the tokens.
+// behind it, in the order of the tokens: a block a unit, a coordinate of a row
+// a thread.
 template <int D, bool P4>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(D * (P4 ? 4 : 8)) paged_merge_kernel(const __grid_constant__ RowsParams p) {
   constexpr int RT = P4 ? 4 : 8;
+  __shared__ float s_y[RT][D], s_top[RT];
+  __shared__ float s_e[RT][32], s_l[RT];
   const PagedAttentionArgs &a = p.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
   const float vs = table_scale(a.vq.centroids, lane);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int4 desc = __ldcg(p.desc + c);
-  if (desc.x == 0) return;
+  const int n = desc.x;
+  if (n == 0) return;
   const int G = a.Hq / a.Hkv;
   const Req req = load_req(a, desc.y, RT, p.faults);
   const int row0 = desc.z * RT, nrows = min(RT, req.n * G - row0);
-  const float vscale = 1.0f / (a.vq.sqrt_d * vs);
-  for (int i = warp; i < nrows; i += 8) {
-    auto slot = [&](int k) {
-      return p.slots + ((size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * kMaxRows + i) * (D + 2);
-    };
+  // piece k's slot
+  auto slot = [&](int k) { return p.slots + (size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * kMaxRows * (D + 2); };
+  if (warp < nrows) {
     float m = -FLT_MAX;
-    for (int k = lane; k < desc.x; k += 32) m = fmaxf(m, __ldcg(slot(k) + D));
+    for (int k = lane; k < n; k += 32) m = fmaxf(m, __ldcg(slot(k) + warp * (D + 2) + D));
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(dev::kFull, m, x));
-    float L = 0.f, y[D / 32];
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) y[e] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < desc.x; ++k) {
-      const float *s = slot(k);
-      const float f = exp2f(__ldcg(s + D) - m);
-      L = fmaf(f, __ldcg(s + D + 1), L);
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) y[e] = fmaf(f, __ldcg(s + lane * (D / 32) + e), y[e]);
+    if (lane == 0) {
+      s_top[warp] = m;
+      s_l[warp] = 0.f;
     }
-    const int qi = (row0 + i) / G;
-    store_out<D>(a, (int64_t)req.q0 + qi, desc.w * G + (row0 + i) - qi * G, lane, y, m, L, vscale);
+  }
+  __syncthreads();
+  const int i = tid / D, k = tid % D;
+  float y = 0.f;
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    if (warp < nrows) {
+      float e = 0.f, l = 0.f;
+      if (k0 + lane < n) {
+        const float *s = slot(k0 + lane) + warp * (D + 2);
+        e = exp2f(__ldcg(s + D) - s_top[warp]);
+        l = e * __ldcg(s + D + 1);
+      }
+      s_e[warp][lane] = e;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(dev::kFull, l, x);
+      if (lane == 0) s_l[warp] += l;
+    }
+    __syncthreads();
+    if (i < nrows) {
+      const int end = min(32, n - k0);
+#pragma unroll 8
+      for (int x = 0; x < end; ++x) y = fmaf(s_e[i][x], __ldcg(slot(k0 + x) + i * (D + 2) + k), y);
+    }
+    __syncthreads();
+  }
+  s_y[i][k] = y;
+  __syncthreads();
+  if (warp < nrows) {
+    float v[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) v[e] = s_y[warp][place<D>(lane * (D / 32) + e)];
+    const int qi = (row0 + warp) / G;
+    store_out<D>(a, (int64_t)req.q0 + qi, desc.w * G + (row0 + warp) - qi * G, lane, v, s_top[warp], s_l[warp],
+                 1.0f / (a.vq.sqrt_d * vs));
   }
 }
 
@@ -672,7 +725,7 @@ cudaError_t run_rows(const RowsParams &p, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at{};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(D * (P4 ? 4 : 8));
   cfg.stream = s;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
@@ -683,7 +736,8 @@ cudaError_t run_rows(const RowsParams &p, cudaStream_t s) {
 
 template <int D>
 cudaError_t run_d(const RowsParams &p, bool p4, cudaStream_t s) {
-  const bool unit = p.a.k.sn == 1 && p.a.v.sn == 1;
+  const CacheView &k = p.a.k, &v = p.a.v;
+  const bool unit = k.sn == 1 && v.sn == 1 && k.sb == v.sb && k.sh == v.sh;
   if (p4) return unit ? run_rows<D, true, true>(p, s) : run_rows<D, true, false>(p, s);
   return unit ? run_rows<D, false, true>(p, s) : run_rows<D, false, false>(p, s);
 }
