@@ -36,21 +36,21 @@ namespace {
 
 using namespace paged;
 
-constexpr int kStep = 16;                // tokens per step
+constexpr int kStep = 32;                // tokens per step, in two halves of 16 that may lie in two pages
 constexpr uint32_t kTabAddr = 0x10000u;  // the pair tables: 64 KiB at this shared address
 constexpr uint32_t kPartAddr = 0x20000u; // the warps' partial sums
 constexpr int kMaxRows = 8;
-constexpr int kStages = 3;               // a warp's steps in shared memory
+constexpr int kStages = 2;               // a warp's steps in shared memory: one worked on, one on its way
 
 template <int D>
 struct Cfg {
 #ifndef RW
-#define RW 16
+#define RW 12
 #endif
   static constexpr int kWarps = RW;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kPitch = D + 4;  // floats of a partial row (no bank clash between rows)
-  // a step: K codes, V codes, 16 norms of each
+  // a step: K codes, V codes, norms of each
   static constexpr int kStepBytes = kStep * D + 2 * kStep * 4;
   static constexpr int kRing = kStages * kStepBytes;
   // rings above the tables (the partial sums reuse the space), the rest below
@@ -86,6 +86,7 @@ struct RowsParams {
 struct Req {
   int q0, n;        // query rows
   int kv;
+  int first;        // the first token that any of its rows sees
   int lo, hi;       // steps [lo, hi)
   int tiles;
 };
@@ -103,7 +104,8 @@ __device__ __forceinline__ Req load_req(const PagedAttentionArgs &a, int r, int 
     q.kv = cap;
   }
   q.tiles = (q.n * (a.Hq / a.Hkv) + rows_per_tile - 1) / rows_per_tile;
-  q.lo = a.window > 0 ? max(q.kv - q.n + 1 - a.window, 0) / kStep : 0;
+  q.first = a.window > 0 ? max(q.kv - q.n + 1 - a.window, 0) : 0;
+  q.lo = q.first / kStep;
   // a request that sees nothing still has one (empty) step, which writes its zeros
   q.hi = max((q.kv + kStep - 1) / kStep, q.lo + 1);
   return q;
@@ -286,9 +288,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
   const float kscale = a.scale * 1.4426950408889634f / (a.kq.sqrt_d * s_scale[0]);
   const float vscale = 1.0f / (a.vq.sqrt_d * s_scale[1]);
 
-  // the lane's 16 bytes of a step's records (of the first 8 tokens for d = 128), and where they go
-  const uint8_t *kc_lane = a.k.codes + 16 * lane, *vc_lane = a.v.codes + 16 * lane;
-  const uint32_t v_to = v_place<D>(lane / (D / 32), lane % (D / 32));
+  // the lane's 16 bytes of a half's records (of its first 8 tokens for d = 128) and its norm, and where they go
+  const int64_t k_tok = a.k.sn * (D / 2), v_tok = a.v.sn * (D / 2);
+  const uint8_t *kc_lane = a.k.codes + (lane / (D / 32)) * k_tok + (lane % (D / 32)) * 16;
+  const uint8_t *vc_lane = a.v.codes + (lane / (D / 32)) * v_tok + (lane % (D / 32)) * 16;
+  const float *n_lane = lane < 16 ? a.k.norms + lane * a.k.sn : a.v.norms + (lane - 16) * a.v.sn;
+  const uint32_t v_to = v_place<D>(lane / (D / 32), lane % (D / 32)), n_to = 4 * (lane & 15) + (lane < 16 ? 0 : 128);
   // and the lane's reads: V of tokens 2 q4 and 2 q4 + 1
   const uint32_t v_at0 = v_place<D>(2 * q4, g * (D / 16) / 16) + (g * (D / 16)) % 16;
   const uint32_t v_at1 = v_place<D>(2 * q4 + 1, g * (D / 16) / 16) + (g * (D / 16)) % 16;
@@ -308,14 +313,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
 
     const int32_t *row = a.table + (int64_t)r * a.table_stride;
     const int n_steps = s1 - s0 > warp ? (s1 - s0 - warp + W - 1) / W : 0;
-    // The records of 8 of the warp's steps, step it + lane % 8 a lane, found a batch ahead; -1 without a page
-    // and behind the piece's last step.
+    // The records of 4 of the warp's steps, half lane % 2 of step it + lane / 2 % 4 a lane, found a batch ahead;
+    // -1 without a page and behind the piece's last step.
     int64_t krec, vrec, krec2, vrec2;
     auto find = [&](int it, int64_t &kr, int64_t &vr) {
-      const int s = s0 + warp + (it + (lane & 7)) * W;
+      const int s = s0 + warp + (it + ((lane >> 1) & 3)) * W;
       kr = vr = -1;
-      const int t0 = s * kStep;
-      if (s < s1 && t0 < req.kv) {
+      const int t0 = s * kStep + 16 * (lane & 1);
+      if (s < s1 && t0 < req.kv && t0 + 16 > req.first) {
         const int page = t0 / a.page_size, off = t0 - page * a.page_size;
         const int id = __ldg(row + page);
         if ((unsigned)id < (unsigned)a.n_pages) {
@@ -326,33 +331,34 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
         }
       }
     };
-    // Step it's records into its stage, asynchronously; bit it % 3 of `ok` says whether there are any.
+    // Step it's records into its stage, asynchronously; bits 2 stage + half of `ok` say whether there are any.
     uint32_t ok = 0;
-    auto issue = [&](int it, int stage) {
-      const int64_t kr = __shfl_sync(dev::kFull, krec, it & 7);
-      const int64_t vr = UNIT ? kr : __shfl_sync(dev::kFull, vrec, it & 7);
+    auto issue = [&](int it) {
+      const int stage = it & 1;
       const uint32_t to = ring + stage * Cfg<D>::kStepBytes;
-      ok = (ok & ~(1u << stage)) | ((kr >= 0 ? 1u : 0u) << stage);
-      if (kr >= 0) {
-        constexpr int CH = D / 32;  // 16-byte words of a record
+      ok &= ~(3u << (2 * stage));
 #pragma unroll
-        for (int i = 0; i < CH / 2; ++i) {
-          const int t = (lane + 32 * i) / CH;
-          const int64_t o = UNIT ? (int64_t)0 : t * (a.k.sn - 1) * (D / 2), u = UNIT ? (int64_t)0 : t * (a.v.sn - 1) * (D / 2);
-          cp_async16(to + 16 * (lane + 32 * i), kc_lane + kr * (D / 2) + o + 512 * i);
-          cp_async16(to + kStep * (D / 2) + v_to + 512 * i, vc_lane + vr * (D / 2) + u + 512 * i);
+      for (int hf = 0; hf < 2; ++hf) {
+        const int64_t kr = __shfl_sync(dev::kFull, krec, 2 * (it & 3) + hf);
+        const int64_t vr = UNIT ? kr : __shfl_sync(dev::kFull, vrec, 2 * (it & 3) + hf);
+        if (kr >= 0) {
+          ok |= 1u << (2 * stage + hf);
+          const uint8_t *ks = kc_lane + kr * (D / 2), *vs = vc_lane + vr * (D / 2);
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) {
+            cp_async16(to + 16 * lane + hf * (8 * D) + 512 * i, ks + (UNIT ? 512 * i : 8 * i * k_tok));
+            cp_async16(to + kStep * (D / 2) + v_to + hf * (8 * D) + 512 * i, vs + (UNIT ? 512 * i : 8 * i * v_tok));
+          }
+          // lanes 0..15 the norms of K, the others those of V
+          cp_async4(to + kStep * D + n_to + 64 * hf, n_lane + (UNIT || lane < 16 ? kr : vr));
         }
-        const int t = lane & 15;
-        cp_async4(to + kStep * D + 4 * lane,
-                  lane < 16 ? a.k.norms + kr + (UNIT ? t : t * a.k.sn) : a.v.norms + vr + (UNIT ? t : t * a.v.sn));
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (n_steps > 0) {
       find(0, krec, vrec);
-      find(8, krec2, vrec2);
-      issue(0, 0);
-      issue(1, 1);
+      find(4, krec2, vrec2);
+      issue(0);
     }
 
     // ---- query rows: sign flips, FWHT, a power of two that brings the largest into [1, 2)
@@ -415,38 +421,40 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 
-    // The running softmax of the lane's rows over its tokens g and 8 + g (value 2 i + o: token 8 i + g, row o):
-    // scores in, weights times value norms out.  M is a reference that moves only when one of them would pass 2^8.
-    auto soft = [&](auto edge, int t0, float (&t)[4], const float (&kn)[2], const float (&vn)[2]) {
+    // The running softmax of the lane's rows over its tokens 8 i + g (value [i][o]: row o): scores in, weights
+    // times value norms out.  M is a reference that moves only when one of them would pass 2^8.
+    auto soft = [&](auto edge, int t0, uint32_t halves, float (&t)[4][2], const float (&kn)[4], const float (&vn)[4]) {
       constexpr bool EDGE = decltype(edge)::value;
-      float lv[2], mx[2], s[4];
-      bool seen[4];
+      float lv[4], s[4][2], mx = -INFINITY;
+      bool seen[4][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const int j = t0 + 8 * i + g;
         lv[i] = fmaxf(log2_approx(vn[i]), -64.f);
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
-          const int e = 2 * i + o;
-          seen[e] = !EDGE || (j >= see_lo[o] && j < see_hi[o] && j < req.kv);
-          s[e] = t[e] * (f[o] * kn[i]);
-          t[e] = s[e] - M[o];
-          if (EDGE && !seen[e]) t[e] = -INFINITY;
+          seen[i][o] = !EDGE || (j >= see_lo[o] && j < see_hi[o] && j < req.kv && (halves >> (i >> 1) & 1));
+          s[i][o] = t[i][o] * (f[o] * kn[i]);
+          t[i][o] = s[i][o] - M[o];
+          if (EDGE && !seen[i][o]) t[i][o] = -INFINITY;
         }
+        mx = fmaxf(mx, fmaxf(t[i][0], t[i][1]) + lv[i]);
       }
-      if (__any_sync(dev::kFull, fmaxf(fmaxf(t[0], t[1]) + lv[0], fmaxf(t[2], t[3]) + lv[1]) > 8.f)) {
+      if (__any_sync(dev::kFull, mx > 8.f)) {
         float r2[2];
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
-          mx[o] = fmaxf(seen[o] ? s[o] + lv[0] : -INFINITY, seen[2 + o] ? s[2 + o] + lv[1] : -INFINITY);
+          float m = -INFINITY;
 #pragma unroll
-          for (int x = 4; x < 32; x <<= 1) mx[o] = fmaxf(mx[o], __shfl_xor_sync(dev::kFull, mx[o], x));
-          const float m2 = fmaxf(M[o], mx[o]);
-          r2[o] = exp2f(M[o] - m2);
-          M[o] = m2;
+          for (int i = 0; i < 4; ++i) m = fmaxf(m, seen[i][o] ? s[i][o] + lv[i] : -INFINITY);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(dev::kFull, m, x));
+          m = fmaxf(M[o], m);
+          r2[o] = exp2f(M[o] - m);
+          M[o] = m;
           l[o] *= r2[o];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) t[2 * i + o] = seen[2 * i + o] ? s[2 * i + o] - m2 : -INFINITY;
+          for (int i = 0; i < 4; ++i) t[i][o] = seen[i][o] ? s[i][o] - m : -INFINITY;
         }
 #pragma unroll
         for (int j = 0; j < MV; ++j)
@@ -454,72 +462,74 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
           for (int e = 0; e < 4; ++e) acc[j][e] *= r2[e & 1];
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        t[e] = exp2_approx(t[e]);
-        l[e & 1] += t[e];
-        t[e] *= vn[e >> 1];
-        if (EDGE && !seen[e]) t[e] = 0.f;
-      }
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          t[i][o] = exp2_approx(t[i][o]);
+          l[o] += t[i][o];
+          t[i][o] *= vn[i];
+          if (EDGE && !seen[i][o]) t[i][o] = 0.f;
+        }
     };
 
-    int stage = 0;
     for (int it = 0; it < n_steps; ++it) {
       const int t0 = (s0 + warp + it * W) * kStep;
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      const uint32_t halves = ok >> (2 * (it & 1)) & 3;
+      const uint32_t from = ring + (it & 1) * Cfg<D>::kStepBytes;
+      asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
-      if (((it + 2) & 7) == 0) {
+      if (((it + 1) & 3) == 0) {
         krec = krec2;
         vrec = vrec2;
-        find(it + 10, krec2, vrec2);
+        find(it + 5, krec2, vrec2);
       }
-      const int at_stage = stage;
-      issue(it + 2, stage == 0 ? 2 : stage - 1);  // the stage of step it - 1
-      stage = stage == 2 ? 0 : stage + 1;
-      if (!(ok >> at_stage & 1)) continue;
-      const uint32_t from = ring + at_stage * Cfg<D>::kStepBytes;
-      uint32_t ck[2][D / 32], cv[4][D / 64];  // K of tokens g, 8 + g; V of 2 q4, 2 q4 + 1, 8 + 2 q4, 9 + 2 q4
-      float kn[2], vn[2];                     // of tokens g, 8 + g
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        lds_words(from + (8 * i + g) * (D / 2) + q4 * (D / 8), ck[i]);
-        kn[i] = lds_f32(from + kStep * D + 4 * (8 * i + g));
-        vn[i] = lds_f32(from + kStep * D + 64 + 4 * (8 * i + g));
-      }
-      // ---- scores: value 2 i + o is token 8 i + g, column 2 q4 + o
+      issue(it + 1);  // into the stage of step it - 1
+      if (!halves) continue;
+      // ---- scores: value 2 x + o of half i is token 16 i + 8 x + g, column 2 q4 + o
       float sc[2][4];
 #pragma unroll
-      for (int c2 = 0; c2 < 2; ++c2)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[c2][e] = 0.f;
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        const uint32_t x = ck[0][w], y = ck[1][w];
-        const uint32_t a0 = pair<0>(x, ktab), a1 = pair<0>(y, ktab), a2 = pair<1>(x, ktab), a3 = pair<1>(y, ktab);
-        const uint32_t b0 = pair<2>(x, ktab), b1 = pair<2>(y, ktab), b2 = pair<3>(x, ktab), b3 = pair<3>(y, ktab);
-#pragma unroll
-        for (int o = 0; o < QS; ++o) {
-          // two chains of sums
-          mma(sc[0], a0, a1, a2, a3, qb[o][2 * w][0], qb[o][2 * w][1]);
-          mma(sc[1], b0, b1, b2, b3, qb[o][2 * w + 1][0], qb[o][2 * w + 1][1]);
-        }
-      }
-      float t[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        t[e] = sc[0][e] + sc[1][e];
-        if (P4) t[e] += __shfl_xor_sync(dev::kFull, t[e], 2);  // the hi and lo columns
-      }
-      if (t0 + kStep > full_hi || t0 < full_lo)
-        soft(std::true_type{}, t0, t, kn, vn);
-      else
-        soft(std::false_type{}, t0, t, kn, vn);
-      // weights to operand words: fp16 pairs of two rows at a token, transposed to two tokens of a row
-      uint32_t pb[QS][2];
+        for (int e = 0; e < 4; ++e) sc[i][e] = 0.f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const __half2 hi = __floats2half2_rn(t[2 * i], t[2 * i + 1]);
+        uint32_t c0[D / 32], c1[D / 32];  // codes of tokens 16 i + g and 16 i + 8 + g
+        lds_words(from + (16 * i + g) * (D / 2) + q4 * (D / 8), c0);
+        lds_words(from + (16 * i + 8 + g) * (D / 2) + q4 * (D / 8), c1);
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          const uint32_t x = c0[w], y = c1[w];
+          const uint32_t a0 = pair<0>(x, ktab), a1 = pair<0>(y, ktab), a2 = pair<1>(x, ktab), a3 = pair<1>(y, ktab);
+          const uint32_t b0 = pair<2>(x, ktab), b1 = pair<2>(y, ktab), b2 = pair<3>(x, ktab), b3 = pair<3>(y, ktab);
+#pragma unroll
+          for (int o = 0; o < QS; ++o) {
+            mma(sc[i], a0, a1, a2, a3, qb[o][2 * w][0], qb[o][2 * w][1]);
+            mma(sc[i], b0, b1, b2, b3, qb[o][2 * w + 1][0], qb[o][2 * w + 1][1]);
+          }
+        }
+      }
+      float t[4][2], kn[4], vn[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        kn[i] = lds_f32(from + kStep * D + 4 * (8 * i + g));
+        vn[i] = lds_f32(from + kStep * D + 128 + 4 * (8 * i + g));
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          t[i][o] = sc[i >> 1][2 * (i & 1) + o];
+          if (P4) t[i][o] += __shfl_xor_sync(dev::kFull, t[i][o], 2);  // the hi and lo columns
+        }
+      }
+      if (t0 + kStep > full_hi || t0 < full_lo || halves != 3)
+        soft(std::true_type{}, t0, halves, t, kn, vn);
+      else
+        soft(std::false_type{}, t0, halves, t, kn, vn);
+      // weights to operand words: fp16 pairs of two rows at a token, transposed to two tokens of a row
+      uint32_t pb[QS][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 hi = __floats2half2_rn(t[i][0], t[i][1]);
         const float2 back = __half22float2(hi);
-        const __half2 lo = __floats2half2_rn(t[2 * i] - back.x, t[2 * i + 1] - back.y);
+        const __half2 lo = __floats2half2_rn(t[i][0] - back.x, t[i][1] - back.y);
         const uint32_t wh = *reinterpret_cast<const uint32_t *>(&hi), wl = *reinterpret_cast<const uint32_t *>(&lo);
         if (P4) {
           pb[0][i] = transpose8(q4 < 2 ? wh : wl);
@@ -528,29 +538,32 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
           pb[QS - 1][i] = transpose8(wl);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        lds_words(from + kStep * (D / 2) + v_at0 + 8 * i * (D / 2), cv[2 * i]);
-        lds_words(from + kStep * (D / 2) + v_at1 + 8 * i * (D / 2), cv[2 * i + 1]);
-      }
       // ---- values: tokens 2 q4 and 2 q4 + 1 interleaved (even and odd coordinates apart)
 #pragma unroll
-      for (int w = 0; w < D / 64; ++w) {
-        const uint32_t x0 = cv[0][w], x1 = cv[1][w], x2 = cv[2][w], x3 = cv[3][w];
-        const uint32_t e0 = (x0 & 0x0f0f0f0fu) | ((x1 << 4) & 0xf0f0f0f0u);
-        const uint32_t o0 = ((x0 >> 4) & 0x0f0f0f0fu) | (x1 & 0xf0f0f0f0u);
-        const uint32_t e1 = (x2 & 0x0f0f0f0fu) | ((x3 << 4) & 0xf0f0f0f0u);
-        const uint32_t o1 = ((x2 >> 4) & 0x0f0f0f0fu) | (x3 & 0xf0f0f0f0u);
-        auto tile = [&](auto k) {
-          constexpr int K = decltype(k)::value;
-          const uint32_t a0 = pair<K>(e0, vtab), a1 = pair<K>(o0, vtab), a2 = pair<K>(e1, vtab), a3 = pair<K>(o1, vtab);
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t vf = from + kStep * (D / 2) + 16 * i * (D / 2);
+        uint32_t c0[D / 64], c1[D / 64], c2[D / 64], c3[D / 64];
+        lds_words(vf + v_at0, c0);
+        lds_words(vf + v_at1, c1);
+        lds_words(vf + 8 * (D / 2) + v_at0, c2);
+        lds_words(vf + 8 * (D / 2) + v_at1, c3);
 #pragma unroll
-          for (int o = 0; o < QS; ++o) mma(acc[4 * w + K], a0, a1, a2, a3, pb[o][0], pb[o][1]);
-        };
-        tile(std::integral_constant<int, 0>{});
-        tile(std::integral_constant<int, 1>{});
-        tile(std::integral_constant<int, 2>{});
-        tile(std::integral_constant<int, 3>{});
+        for (int w = 0; w < D / 64; ++w) {
+          const uint32_t e0 = (c0[w] & 0x0f0f0f0fu) | ((c1[w] << 4) & 0xf0f0f0f0u);
+          const uint32_t o0 = ((c0[w] >> 4) & 0x0f0f0f0fu) | (c1[w] & 0xf0f0f0f0u);
+          const uint32_t e1 = (c2[w] & 0x0f0f0f0fu) | ((c3[w] << 4) & 0xf0f0f0f0u);
+          const uint32_t o1 = ((c2[w] >> 4) & 0x0f0f0f0fu) | (c3[w] & 0xf0f0f0f0u);
+          auto tile = [&](auto k) {
+            constexpr int K = decltype(k)::value;
+            const uint32_t a0 = pair<K>(e0, vtab), a1 = pair<K>(o0, vtab), a2 = pair<K>(e1, vtab), a3 = pair<K>(o1, vtab);
+#pragma unroll
+            for (int o = 0; o < QS; ++o) mma(acc[4 * w + K], a0, a1, a2, a3, pb[o][2 * i], pb[o][2 * i + 1]);
+          };
+          tile(std::integral_constant<int, 0>{});
+          tile(std::integral_constant<int, 1>{});
+          tile(std::integral_constant<int, 2>{});
+          tile(std::integral_constant<int, 3>{});
+        }
       }
     }
     // all copies of this warp are in, and every warp is through with its ring before the sums go there
