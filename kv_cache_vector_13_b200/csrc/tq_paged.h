@@ -85,5 +85,8 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs &a, cudaStream_t s);
 // d = 64 and 128 on tensor cores, a few query rows a unit (tq_paged_rows.cu)
 size_t paged_rows_workspace(int d);
 cudaError_t launch_paged_rows(const PagedAttentionArgs &a, cudaStream_t s);
+// d = 64 and 128 on the fifth-generation tensor cores, 128 or 256 query rows a unit (tq_paged_tile.cu)
+size_t paged_tile_workspace(int R, int64_t T, int Hq, int Hkv, int d);
+cudaError_t launch_paged_tile(const PagedAttentionArgs &a, cudaStream_t s);
 
 }  // namespace tq

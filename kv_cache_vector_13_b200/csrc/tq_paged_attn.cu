@@ -193,11 +193,14 @@ cudaError_t run_general(const GeneralParams &p, cudaStream_t s) {
 }  // namespace
 
 size_t paged_attention_workspace(int R, int64_t T, int Hq, int Hkv, int d) {
-  return d == 256 ? 16 : paged_rows_workspace(d);
+  if (d == 256) return 16;
+  const size_t rows = paged_rows_workspace(d), tile = paged_tile_workspace(R, T, Hq, Hkv, d);
+  return rows > tile ? rows : tile;
 }
 
 cudaError_t launch_paged_attention(const PagedAttentionArgs &a, cudaStream_t s) {
-  if (a.kq.d != 256) return launch_paged_rows(a, s);
+  if (a.kq.d != 256)
+    return (int64_t)a.max_q * (a.Hq / a.Hkv) <= 8 ? launch_paged_rows(a, s) : launch_paged_tile(a, s);
   GeneralParams p{a, nullptr};
   const cudaError_t e = fault_word(&p.faults);
   if (e != cudaSuccess) return e;

@@ -1,0 +1,929 @@
+// Attention of many query rows a request over a paged 4-bit cache (sm_100a):
+// prefill, and decode with more rows a KV head than the small tiles take.
+//
+// A unit is (request, KV head, tile of query rows), a block 128 cached tokens.
+// All units' blocks form one line cut evenly over one persistent CTA an SM;
+// units cut by a range's end leave partial sums that a last kernel merges in
+// the order of the tokens.
+//
+// Per block, on the fifth-generation tensor cores: S = Q K^T and O += P V with
+// fp16 operands and fp32 sums in tensor memory.  Roles of a CTA's 13 warps:
+//   * 4 warps decode: a token's 64 code bytes become 128 fp16 centroids in the
+//     operand tile, a code byte (two codes) being one read of a table of
+//     centroid pairs, one copy per lane, whose address is one byte permute.
+//     K and V tiles have the same layout, a token's 8 coordinates a 16-byte
+//     row: K-major for the scores, and for the values, whose sum runs over
+//     tokens, the transposed operand form.  No V transpose is ever made.
+//   * 2 x 4 warps softmax, a query row a thread: scores from tensor memory
+//     times ||k||, the running reference and sum, weights times ||v|| back
+//     into tensor memory as the next product's operand.
+//   * 1 thread issues the products.
+// Two sets of rows (or of blocks) alternate, so that one's products run while
+// the other's softmax does:
+//   wide:  256 rows a tile, both halves against every block (bf16 outputs;
+//          operands rounded once, 2^-11 against the output's 2^-8);
+//   split: 128 rows a tile, even blocks to one set, odd ones to the other,
+//          which are merged at the end (few rows a unit); with HL the rows and
+//          weights are fp16 pairs hi + lo, two products each (fp16 outputs).
+
+#include "../../include/tq.h"
+#include "tq_device.cuh"
+#include "tq_paged.h"
+#include "tq_paged_dev.cuh"
+#include "tq_umma.cuh"
+
+#include <float.h>
+#include <type_traits>
+
+namespace tq {
+namespace {
+
+using namespace paged;
+
+constexpr int kBlk = 128;                 // tokens per block
+constexpr int kThreads = 416;             // 2 x 4 softmax warps, 4 decode warps, 1 for the products
+constexpr uint32_t kTabAddr = 0x10000u;   // the pair tables: 64 KiB at this shared address
+constexpr uint32_t kHighAddr = 0x20000u;  // V, K and the second query tile
+
+template <int D>
+struct Tile {
+  static constexpr int kGroup = (D / 8) * 128;         // bytes of 8 rows: D / 8 core matrices
+  static constexpr int kBytes = (kBlk / 8) * kGroup;   // an operand tile of 128 rows
+};
+
+struct TileParams {
+  PagedAttentionArgs a;
+  int rt;                  // rows per tile: 256 wide, 128 split
+  const __half *qhi, *qlo; // [T * Hq][D] turned rows
+  const float *qf;         // [T * Hq] the factor their scores still need (softmax scale, log2 e, row scale)
+  int32_t *first;          // [R + 1] first tile of each request
+  int64_t *line;           // [tiles + 1] blocks (of one KV head) before each tile
+  float *slots;            // [2 * ctas][rt * (D + 2)]
+  int4 *desc;              // [ctas]
+  unsigned *faults;
+};
+
+struct Req {
+  int q0, n, kv;
+};
+
+__device__ __forceinline__ Req load_req(const PagedAttentionArgs &a, int r, unsigned *faults) {
+  Req q;
+  q.q0 = max(a.cu_q ? __ldg(a.cu_q + r) : r, 0);
+  const int q1 = a.cu_q ? __ldg(a.cu_q + r + 1) : r + 1;
+  q.n = max(min(q1, (int)a.T) - q.q0, 0);
+  q.kv = max(__ldg(a.kv_lens + r), 0);
+  const int cap = a.max_pages * a.page_size;
+  if (q.kv > cap) {
+    atomicOr(faults, kFaultIndex);
+    q.kv = cap;
+  }
+  return q;
+}
+
+// Blocks [b0, b1) that any row of tile i of a request sees; one (empty) block
+// for rows that see nothing, which writes their zeros.
+__device__ __forceinline__ void tile_blocks(const PagedAttentionArgs &a, const Req &q, int rt, int i, int &b0, int &b1,
+                                            int &first) {
+  const int G = a.Hq / a.Hkv;
+  const int p0 = q.kv - q.n + i * rt / G, p1 = q.kv - q.n + (min((i + 1) * rt, q.n * G) - 1) / G;
+  const int hi = a.causal ? max(p1 + 1, 0) : q.kv;
+  first = a.window > 0 ? max(p0 + 1 - a.window, 0) : 0;
+  b0 = first / kBlk;
+  b1 = max((hi + kBlk - 1) / kBlk, b0 + 1);
+}
+
+// ------------------------------------------------- query rows and schedule
+
+template <int N>
+__device__ __forceinline__ int64_t scan(int64_t v, int64_t *s_warp, int64_t *total) {  // exclusive, N threads
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(dev::kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[w] = x;
+  __syncthreads();
+  int64_t base = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < N / 32; ++i) {
+    if (i < w) base += s_warp[i];
+    all += s_warp[i];
+  }
+  __syncthreads();
+  *total = all;
+  return base + x - v;
+}
+
+// Block 0 lays out the line; the others turn the query rows: sign flips, FWHT
+// (16 coordinates a lane), a power of two that brings the largest into [1, 2).
+template <int D, bool HL>
+__global__ void __launch_bounds__(256) paged_tile_prep_kernel(const __grid_constant__ TileParams p) {
+  const PagedAttentionArgs &a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  if (blockIdx.x == 0) {
+    __shared__ int64_t s_warp[8];
+    const int G = a.Hq / a.Hkv;
+    int64_t tiles = 0;
+    for (int r0 = 0; r0 < a.R; r0 += 256) {
+      const int r = r0 + tid;
+      int64_t mine = 0, all;
+      if (r < a.R) {
+        const Req q = load_req(a, r, p.faults);
+        mine = ((int64_t)q.n * G + p.rt - 1) / p.rt;
+      }
+      const int64_t before = tiles + scan<256>(mine, s_warp, &all);
+      if (r < a.R) p.first[r] = (int32_t)before;
+      tiles += all;
+    }
+    if (tid == 0) p.first[a.R] = (int32_t)tiles;
+    __syncthreads();  // the block reads what it wrote
+    int64_t blocks = 0;
+    for (int64_t t0 = 0; t0 < tiles; t0 += 256) {
+      const int64_t t = t0 + tid;
+      int64_t mine = 0, all;
+      if (t < tiles) {
+        int i = 0, j = a.R;  // the last request i with first[i] <= t
+        while (j - i > 1) {
+          const int m = (i + j) >> 1;
+          if (p.first[m] <= t) i = m; else j = m;
+        }
+        int b0, b1, first;
+        tile_blocks(a, load_req(a, i, p.faults), p.rt, (int)t - p.first[i], b0, b1, first);
+        mine = b1 - b0;
+      }
+      const int64_t before = blocks + scan<256>(mine, s_warp, &all);
+      if (t < tiles) p.line[t] = before;
+      blocks += all;
+    }
+    if (tid == 0) p.line[tiles] = blocks;
+    return;
+  }
+  constexpr int E = 16, T = D / E, RPW = 32 / T;
+  const int t = lane % T;
+  const int64_t rows = a.T * a.Hq;
+  const float scale = a.scale * 1.4426950408889634f / (a.kq.sqrt_d * table_scale(a.kq.centroids, lane));
+  uint32_t sg = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) sg |= (a.kq.signs[t * E + e] < 0 ? 1u : 0u) << e;
+  for (int64_t r0 = ((int64_t)(blockIdx.x - 1) * 8 + warp) * RPW; r0 < rows; r0 += (int64_t)(gridDim.x - 1) * 8 * RPW) {
+    int64_t row = r0 + lane / T;
+    const bool active = row < rows;
+    if (!active) row = r0;
+    const int64_t tok = row / a.Hq;
+    const int hq = (int)(row - tok * a.Hq);
+    const uint16_t *src = static_cast<const uint16_t *>(a.q) + tok * a.q_st + hq * a.q_sh + t * E;
+    float x[E];
+    if (a.dtype == TQ_BF16) dev::load_block<TQ_BF16, E>(src, x);
+    else dev::load_block<TQ_F16, E>(src, x);
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = __uint_as_float(__float_as_uint(x[e]) ^ ((sg >> e & 1u) << 31));
+    dev::fwht<T, E>(x, t);
+    unsigned m = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = T / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(dev::kFull, m, o));
+    const unsigned ex = m >> 23;
+    const float f = ex == 255u || m == 0 ? 1.0f : __uint_as_float(min(max(254u - ex, 1u), 252u) << 23);
+    uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      const float u = x[2 * e] * f, v = x[2 * e + 1] * f;
+      const __half2 h = __floats2half2_rn(u, v);
+      hi[e] = *reinterpret_cast<const uint32_t *>(&h);
+      if (HL) {
+        const float2 b = __half22float2(h);
+        const __half2 l = __floats2half2_rn(u - b.x, v - b.y);
+        lo[e] = *reinterpret_cast<const uint32_t *>(&l);
+      }
+    }
+    if (active) {
+      uint4 *o = reinterpret_cast<uint4 *>(const_cast<__half *>(p.qhi) + row * D + t * E);
+      o[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      o[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+      if (HL) {
+        o = reinterpret_cast<uint4 *>(const_cast<__half *>(p.qlo) + row * D + t * E);
+        o[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        o[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+      }
+      if (t == 0) const_cast<float *>(p.qf)[row] = scale / f;
+    }
+  }
+}
+
+// ------------------------------------------------------------ main kernel
+
+struct Piece {
+  int r, h, row0, nrows, q0, n, kv, first;
+  int b0, b1;        // blocks
+  int starts, ends;  // whether they hold the unit's first and last block
+};
+
+struct Low {
+  uint64_t k_full, k_free, v_full, v_free, n_full[2], s_full[2], p_full[2], o_fin[2];
+  uint32_t tmem, pad;
+  Piece piece;
+  alignas(16) float kn[2][kBlk], vn[2][kBlk], lv[2][kBlk];  // of a block's tokens: ||k||, ||v||, max(log2 ||v||, -64)
+  alignas(16) uint32_t valid[2][kBlk / 32];     // tokens with a record
+  float f[256];                                 // score factors of the rows
+  float m[128], l[128];                         // the odd set's references and sums (split)
+  float scale[2];
+};
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+// Table read of byte k of w: shared address {lane, byte k, table}.
+template <int K>
+__device__ __forceinline__ uint32_t pair(uint32_t w, uint32_t base) {
+  uint32_t a;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(a) : "r"(w), "r"(base), "n"(0x7604 | (K << 4)));
+  return lds32(a);
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// D[tmem] (+)= A[tmem] B for one K = 16 step.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
+  const uint32_t z = 0u;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n}\n" ::"r"(d),
+      "r"(at), "l"(bdesc), "r"(idesc), "r"(accum), "r"(z), "r"(z), "r"(z), "r"(z));
+}
+
+#define TQ_LIST16(v, b) "r"(v[b]), "r"(v[b + 1]), "r"(v[b + 2]), "r"(v[b + 3]), "r"(v[b + 4]), "r"(v[b + 5]), \
+    "r"(v[b + 6]), "r"(v[b + 7]), "r"(v[b + 8]), "r"(v[b + 9]), "r"(v[b + 10]), "r"(v[b + 11]), "r"(v[b + 12]), \
+    "r"(v[b + 13]), "r"(v[b + 14]), "r"(v[b + 15])
+__device__ __forceinline__ void st16(uint32_t t, const uint32_t (&v)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+               "%13, %14, %15};" ::TQ_LIST16(v, 0), "r"(t) : "memory");
+}
+__device__ __forceinline__ void st32(uint32_t t, const uint32_t (&v)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+               "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::
+                   TQ_LIST16(v, 0), TQ_LIST16(v, 16), "r"(t) : "memory");
+}
+__device__ __forceinline__ void ld8(uint32_t t, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(t));
+}
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+template <int D, bool SPLIT, bool HL>
+__global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_constant__ TileParams p) {
+  static_assert(SPLIT || !HL, "pairs of operands only with split blocks");
+  constexpr int RT = SPLIT ? 128 : 256;
+  constexpr int GB = Tile<D>::kGroup, TB = Tile<D>::kBytes;
+  constexpr uint32_t kV = kHighAddr, kK = kHighAddr + TB, kQ1 = kHighAddr + 2 * TB, kQ0 = kTabAddr - TB;
+  constexpr uint32_t kIdS = umma::idesc_f16(128, kBlk), kIdO = umma::idesc_f16(128, D) | (1u << 16);
+  constexpr int NC = D / 32;  // 32-column runs of O
+  extern __shared__ __align__(16) unsigned char s_raw[];
+  Low &sm = *reinterpret_cast<Low *>(s_raw);
+  const PagedAttentionArgs &a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
+  const int G = a.Hq / a.Hkv;
+  const uint32_t dyn = (uint32_t)__cvta_generic_to_shared(s_raw);
+  uint32_t dyn_bytes;
+  asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn_bytes));
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  if (dyn + sizeof(Low) > kQ0 || dyn + dyn_bytes < kQ1 + TB) {
+    if (tid == 0) {
+      atomicOr(p.faults, kFaultSmemLayout);
+      p.desc[c] = make_int4(0, 0, 0, 0);
+    }
+    return;
+  }
+  auto bar = [&](const uint64_t &b) { return (uint32_t)__cvta_generic_to_shared(&b); };
+
+  // ---- the tables (see the rows kernel), barriers, tensor memory
+  uint32_t *pairs = reinterpret_cast<uint32_t *>(s_raw + (kHighAddr - dyn));
+  if (warp < 2) {
+    const float *cent = warp == 0 ? a.kq.centroids : a.vq.centroids;
+    const float s = table_scale(cent, lane);
+    if (lane == 0) sm.scale[warp] = s;
+    for (int e = lane; e < 256; e += 32) {
+      const __half2 h = __floats2half2_rn(s * __ldg(cent + (e & 15)), s * __ldg(cent + (e >> 4)));
+      pairs[warp * 256 + e] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+  }
+  if (warp == 12) umma::alloc(&sm.tmem, 512);
+  if (tid == 0) {
+    umma::mbar_init(bar(sm.k_full), 128);
+    umma::mbar_init(bar(sm.v_full), 128);
+    umma::mbar_init(bar(sm.k_free), 1);
+    umma::mbar_init(bar(sm.v_free), 1);
+    for (int x = 0; x < 2; ++x) {
+      umma::mbar_init(bar(sm.n_full[x]), 128);
+      umma::mbar_init(bar(sm.p_full[x]), 128);
+      umma::mbar_init(bar(sm.s_full[x]), 1);
+      umma::mbar_init(bar(sm.o_fin[x]), 1);
+    }
+  }
+  __syncthreads();
+  {
+    uint4 *tab = reinterpret_cast<uint4 *>(s_raw + (kTabAddr - dyn));
+    for (int i = tid; i < 256 * 16; i += kThreads) {
+      const uint32_t w = pairs[((i >> 3) & 1) * 256 + (i >> 4)];
+      tab[i] = make_uint4(w, w, w, w);
+    }
+  }
+  umma::fence_before();
+  __syncthreads();
+  umma::fence_after();
+  const uint32_t tmem = sm.tmem;
+  // columns: scores (and weights) of set 0 and 1, outputs of set 0 and 1
+  auto s_col = [&](int x) { return tmem + 128 * x; };
+  auto o_col = [&](int x) { return tmem + 256 + 128 * x; };
+
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the line and the turned rows
+  const int tiles = __ldcg(p.first + a.R);
+  const int64_t total = tiles > 0 ? __ldcg(p.line + tiles) * a.Hkv : 0;
+  const int ctas = (int)min((int64_t)gridDim.x, total);
+  int64_t at = c < ctas ? total * c / ctas : 0;
+  const int64_t end = c < ctas ? total * (c + 1) / ctas : 0;
+  int4 desc = make_int4(0, 0, 0, 0);
+
+  // blocks and items (a block for a set) that were done before, for the barriers' phases
+  uint32_t blocks_done = 0, items_done[2] = {0, 0}, pieces_done[2] = {0, 0};
+  bool dead = false;
+  auto wait = [&](const uint64_t &b, uint32_t phase) {
+    if (!dead) dead = !umma::mbar_wait_bounded(bar(b), phase & 1, p.faults, kFaultTimeout);
+  };
+
+  int r = -1, h = 0, tile = 0, ta = 0, tb = 0;  // the unit (thread 0)
+  Req req{};
+  while (at < end) {
+    // ---- the piece: one thread finds the first and walks on from unit to unit
+    if (tid == 0) {
+      int skip = 0;  // blocks of the unit in front of the range
+      if (r < 0) {
+        int i = 0, j = a.R;  // the last request whose line starts at or before `at`
+        while (j - i > 1) {
+          const int m = (i + j) >> 1;
+          if (__ldcg(p.line + __ldcg(p.first + m)) * a.Hkv <= at) i = m; else j = m;
+        }
+        r = i;
+        ta = __ldcg(p.first + r);
+        tb = __ldcg(p.first + r + 1);
+        const int64_t la = __ldcg(p.line + ta), per = __ldcg(p.line + tb) - la, x = at - la * a.Hkv;
+        h = (int)(x / per);
+        const int64_t y = la + (x - (int64_t)h * per);
+        i = ta, j = tb;  // the last tile that starts at or before y
+        while (j - i > 1) {
+          const int m = (i + j) >> 1;
+          if (__ldcg(p.line + m) <= y) i = m; else j = m;
+        }
+        tile = i;
+        skip = (int)(y - __ldcg(p.line + i));
+        req = load_req(a, r, p.faults);
+      } else if (++tile == tb) {
+        tile = ta;
+        if (++h == a.Hkv) {
+          h = 0;
+          do {
+            ++r;
+            ta = tb;
+            tb = __ldcg(p.first + r + 1);
+          } while (tb == ta && r + 1 < a.R);
+          tile = ta;
+          req = load_req(a, r, p.faults);
+        }
+      }
+      Piece q;
+      int b0, b1;
+      tile_blocks(a, req, RT, tile - ta, b0, b1, q.first);
+      q.r = r;
+      q.h = h;
+      q.q0 = req.q0;
+      q.n = req.n;
+      q.kv = req.kv;
+      q.row0 = (tile - ta) * RT;
+      q.nrows = min(RT, req.n * G - q.row0);
+      q.b0 = b0 + skip;
+      q.b1 = (int)min((int64_t)b1, q.b0 + (end - at));
+      q.starts = skip == 0;
+      q.ends = q.b1 == b1;
+      sm.piece = q;
+      if (q.starts && !q.ends) {
+        const int64_t last = at + (b1 - b0) - 1;
+        int64_t e = last * ctas / total;
+        while (e < ctas - 1 && total * (e + 1) / ctas <= last) ++e;
+        while (e > c && total * e / ctas > last) --e;
+        desc = make_int4((int)e - c + 1, r, tile - ta, h);
+      }
+    }
+    __syncthreads();
+    const Piece q = sm.piece;
+    const int nblk = q.b1 - q.b0;
+    // ---- query rows into the operand tiles: 16-byte words of 8 coordinates
+    for (int i = tid; i < RT * (D / 8); i += kThreads) {
+      const int row = i / D * 8 + (i & 7), w = (i >> 3) % (D / 8);
+      uint4 x = make_uint4(0, 0, 0, 0), y = x;
+      if (row < q.nrows) {
+        const int qi = (q.row0 + row) / G;
+        const int64_t src = (int64_t)(q.q0 + qi) * a.Hq + q.h * G + (q.row0 + row - qi * G);
+        x = __ldcg(reinterpret_cast<const uint4 *>(p.qhi + src * D) + w);
+        if (HL) y = __ldcg(reinterpret_cast<const uint4 *>(p.qlo + src * D) + w);
+        if (w == 0) sm.f[row] = __ldcg(p.qf + src);
+      } else if (w == 0) {
+        sm.f[row] = 0.f;
+      }
+      const uint32_t o = ((row & 127) >> 3) * GB + w * 128 + (row & 7) * 16;
+      sts128((row < 128 ? kQ0 : kQ1) + o, x.x, x.y, x.z, x.w);
+      if (HL) sts128(kQ1 + o, y.x, y.y, y.z, y.w);
+    }
+    umma::fence_async_smem();
+    __syncthreads();
+
+    // sets at work, items of each; item k of the piece: block k / 2 (wide, both sets) or k (split)
+    const bool both = SPLIT ? nblk > 1 : q.nrows > 128;
+    const int items = SPLIT || !both ? nblk : 2 * nblk;
+    auto set_of = [&](int k) { return both ? k & 1 : 0; };
+    auto blk_of = [&](int k) { return SPLIT || !both ? k : k >> 1; };
+
+    if (warp == 12) {
+      // ================= products
+      if (lane == 0) {
+        uint32_t n_x[2] = {items_done[0], items_done[1]};
+        auto scores = [&](int k) {
+          const int x = set_of(k), b = blk_of(k);
+          if (SPLIT || !both || x == 0) wait(sm.k_full, blocks_done + b);
+          umma::fence_after();
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint64_t kd = umma::desc(kK + s * 256, 128, GB);
+            if (HL) {
+              umma::mma_f16(s_col(x), umma::desc(kQ0 + s * 256, 128, GB), kd, kIdS, s > 0);
+              umma::mma_f16(s_col(x), umma::desc(kQ1 + s * 256, 128, GB), kd, kIdS, 1);
+            } else {
+              umma::mma_f16(s_col(x), umma::desc((SPLIT || x == 0 ? kQ0 : kQ1) + s * 256, 128, GB), kd, kIdS, s > 0);
+            }
+          }
+          umma::commit(bar(sm.s_full[x]));
+          if (SPLIT || !both || x == 1) umma::commit(bar(sm.k_free));
+        };
+        scores(0);
+        if (both) scores(1);
+        for (int k = 0; k < items; ++k) {
+          const int x = set_of(k), b = blk_of(k);
+          if (SPLIT || !both || x == 0) wait(sm.v_full, blocks_done + b);
+          wait(sm.p_full[x], n_x[x]);
+          umma::fence_after();
+          const bool first = k < (both ? 2 : 1);
+#pragma unroll
+          for (int s = 0; s < kBlk / 16; ++s) {
+            const uint64_t vd = umma::desc(kV + s * 2 * GB, GB, 128);
+            const uint32_t pc = s_col(x) + 32 * (s >> 1) + 8 * (s & 1);
+            mma_ts(o_col(x), pc, vd, kIdO, !first || s > 0);
+            if (HL) mma_ts(o_col(x), pc + 16, vd, kIdO, 1);
+          }
+          if (SPLIT || !both || x == 1) umma::commit(bar(sm.v_free));
+          if (k + (both ? 2 : 1) >= items) umma::commit(bar(sm.o_fin[x]));
+          ++n_x[x];
+          // the set's next scores go where its weights were: behind their product
+          const int next = k + (both ? 2 : 1);
+          if (next < items) scores(next);
+        }
+      }
+      __syncwarp();
+    } else if (warp >= 8) {
+      // ================= codes to operands: 32 tokens of a block a warp, a 16-byte word of each a lane
+      constexpr int TPI = D == 128 ? 8 : 16;   // tokens per pass
+      constexpr int IT = 32 / TPI;
+      const int wq = warp - 8, tk = lane % TPI, ch = lane / TPI;
+      uint32_t ktab, vtab;
+      asm("mov.b32 %0, %1;" : "=r"(ktab) : "r"(kTabAddr + 4 * lane));
+      asm("mov.b32 %0, %1;" : "=r"(vtab) : "r"(kTabAddr + 4 * lane + 128));
+      const int32_t *row = a.table + (int64_t)q.r * a.table_stride;
+      uint4 kc[IT], vc[IT];
+      float kn = 0.f, vn = 0.f;  // of token 32 wq + lane
+      bool have = false;
+      auto record = [&](int j, int64_t &kr, int64_t &vr) {
+        kr = vr = -1;
+        if (j >= q.first && j < q.kv) {
+          const int page = j / a.page_size, off = j - page * a.page_size;
+          const int id = __ldg(row + page);
+          if ((unsigned)id < (unsigned)a.n_pages) {
+            kr = id * a.k.sb + q.h * a.k.sh + off * a.k.sn;
+            vr = id * a.v.sb + q.h * a.v.sh + off * a.v.sn;
+          } else {
+            atomicOr(p.faults, kFaultIndex);
+          }
+        }
+      };
+      auto load = [&](int b) {
+        // the record of token 32 wq + lane; the lanes' tokens of each pass come from there
+        int64_t kr, vr;
+        record(b * kBlk + 32 * wq + lane, kr, vr);
+        have = kr >= 0;
+        kn = have ? __ldg(a.k.norms + kr) : 0.f;
+        vn = have ? __ldg(a.v.norms + vr) : 0.f;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int64_t k1 = __shfl_sync(dev::kFull, kr, TPI * i + tk), v1 = __shfl_sync(dev::kFull, vr, TPI * i + tk);
+          kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
+          if (k1 >= 0) {
+            kc[i] = __ldg(reinterpret_cast<const uint4 *>(a.k.codes + k1 * (D / 2)) + ch);
+            vc[i] = __ldg(reinterpret_cast<const uint4 *>(a.v.codes + v1 * (D / 2)) + ch);
+          }
+        }
+      };
+      auto decode = [&](uint32_t tile, uint32_t tab, const uint4 (&x)[IT]) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int t = 32 * wq + TPI * i + tk;
+          const uint32_t to = tile + (t >> 3) * GB + ch * 4 * 128 + (t & 7) * 16;
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            sts128(to + 128 * j, pair<0>(w[j], tab), pair<1>(w[j], tab), pair<2>(w[j], tab), pair<3>(w[j], tab));
+        }
+      };
+      load(q.b0);
+      for (int b = 0; b < nblk; ++b) {
+        const uint32_t u = blocks_done + b;
+        const int nb = u & 1;
+        // free: the products of the buffer's last block, u - 2, were done before V of block u - 1 was written
+        sm.kn[nb][32 * wq + lane] = kn;
+        sm.vn[nb][32 * wq + lane] = vn;
+        sm.lv[nb][32 * wq + lane] = fmaxf(log2_approx(vn), -64.f);
+        const unsigned ok = __ballot_sync(dev::kFull, have);
+        if (lane == 0) sm.valid[nb][wq] = ok;
+        arrive(bar(sm.n_full[nb]));
+        if (u > 0) wait(sm.k_free, u - 1);
+        decode(kK, ktab, kc);
+        umma::fence_async_smem();
+        arrive(bar(sm.k_full));
+        if (u > 0) wait(sm.v_free, u - 1);
+        decode(kV, vtab, vc);
+        umma::fence_async_smem();
+        arrive(bar(sm.v_full));
+        if (b + 1 < nblk) load(q.b0 + b + 1);
+      }
+    } else {
+      // ================= softmax: set x, a row a thread
+      const int x = warp >> 2, row = (warp & 3) * 32 + lane;
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const int i = SPLIT ? row : 128 * x + row;  // row of the tile
+      const bool live = i < q.nrows;
+      int see_lo = 0, see_hi = INT_MAX;  // rows that are not there see everything (and go nowhere)
+      if (live) {
+        const int pos = q.kv - q.n + (q.row0 + i) / G;
+        see_hi = a.causal ? max(pos + 1, 0) : q.kv;
+        see_lo = a.window > 0 ? max(pos + 1 - a.window, 0) : 0;
+      }
+      const float f = sm.f[i];
+      float M = -FLT_MAX, l = 0.f;
+      const int mine = x < (both ? 2 : 1) ? (SPLIT ? (both ? (nblk + 1 - x) / 2 : nblk) : nblk) : 0;
+      for (int k = 0; k < mine; ++k) {
+        const int b = SPLIT && both ? 2 * k + x : k;
+        const uint32_t u = blocks_done + b;
+        const int nb = u & 1, j0 = (q.b0 + b) * kBlk;
+        wait(sm.n_full[nb], u >> 1);
+        wait(sm.s_full[x], items_done[x] + k);
+        umma::fence_after();
+        const uint4 vm = *reinterpret_cast<const uint4 *>(sm.valid[nb]);
+        const uint32_t valid[4] = {vm.x, vm.y, vm.z, vm.w};
+        const bool whole = see_lo <= j0 && see_hi >= j0 + kBlk && (vm.x & vm.y & vm.z & vm.w) == ~0u;
+        const bool edge = !__all_sync(dev::kFull, whole);
+        auto mask = [&](int r) {  // tokens of run r that the row sees
+          const int lo = max(see_lo - j0 - 32 * r, 0), hi = min(see_hi - j0 - 32 * r, 32);
+          const uint32_t m = hi <= 0 || lo >= 32 ? 0u : (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
+          return m & valid[r];
+        };
+        // the largest logit + log2 ||v||, relative to `ref`
+        auto top = [&](float ref) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            uint32_t s[32];
+            umma::ld32(s_col(x) + lanes + 32 * r, s);
+            umma::wait_ld();
+            const uint32_t m = edge ? mask(r) : ~0u;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 kn = *reinterpret_cast<const float4 *>(&sm.kn[nb][32 * r + e]);
+              const float4 lv = *reinterpret_cast<const float4 *>(&sm.lv[nb][32 * r + e]);
+              const float t0 = fmaf(__uint_as_float(s[e]), kn.x * f, lv.x - ref);
+              const float t1 = fmaf(__uint_as_float(s[e + 1]), kn.y * f, lv.y - ref);
+              const float t2 = fmaf(__uint_as_float(s[e + 2]), kn.z * f, lv.z - ref);
+              const float t3 = fmaf(__uint_as_float(s[e + 3]), kn.w * f, lv.w - ref);
+              if (edge) {
+                if (m >> e & 1) mx = fmaxf(mx, t0);
+                if (m >> (e + 1) & 1) mx = fmaxf(mx, t1);
+                if (m >> (e + 2) & 1) mx = fmaxf(mx, t2);
+                if (m >> (e + 3) & 1) mx = fmaxf(mx, t3);
+              } else {
+                mx = fmaxf(mx, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)));
+              }
+            }
+          }
+          return mx;
+        };
+        // M is a reference that moves only when a weight times its norm would pass 2^8
+        const float rel = k == 0 ? INFINITY : top(M);
+        if (__any_sync(dev::kFull, rel > 8.f)) {
+          const float m2 = fmaxf(M, top(0.f)), r2 = exp2f(M - m2);
+          M = m2;
+          l *= r2;
+          if (k > 0) {  // the scores' barrier says that the products before them are done, those into O too
+#pragma unroll
+            for (int r = 0; r < NC; ++r) {
+              uint32_t o[32];
+              umma::ld32(o_col(x) + lanes + 32 * r, o);
+              umma::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r2);
+              st32(o_col(x) + lanes + 32 * r, o);
+            }
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          uint32_t s[32], w[16], wl[16];
+          umma::ld32(s_col(x) + lanes + 32 * r, s);
+          umma::wait_ld();
+          const uint32_t m = edge ? mask(r) : ~0u;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 kn = *reinterpret_cast<const float4 *>(&sm.kn[nb][32 * r + e]);
+            const float4 vn = *reinterpret_cast<const float4 *>(&sm.vn[nb][32 * r + e]);
+            const float kk[4] = {kn.x, kn.y, kn.z, kn.w}, vv[4] = {vn.x, vn.y, vn.z, vn.w};
+            float t[4];
+#pragma unroll
+            for (int o = 0; o < 4; ++o) {
+              t[o] = exp2_approx(fmaf(__uint_as_float(s[e + o]), kk[o] * f, -M));
+              if (edge && !(m >> (e + o) & 1)) t[o] = 0.f;
+            }
+            l += (t[0] + t[1]) + (t[2] + t[3]);
+#pragma unroll
+            for (int o = 0; o < 4; ++o) t[o] = edge && !(m >> (e + o) & 1) ? 0.f : t[o] * vv[o];
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const __half2 h = __floats2half2_rn(t[2 * o], t[2 * o + 1]);
+              w[e / 2 + o] = *reinterpret_cast<const uint32_t *>(&h);
+              if (HL) {
+                const float2 back = __half22float2(h);
+                const __half2 lo = __floats2half2_rn(t[2 * o] - back.x, t[2 * o + 1] - back.y);
+                wl[e / 2 + o] = *reinterpret_cast<const uint32_t *>(&lo);
+              }
+            }
+          }
+          st16(s_col(x) + lanes + 32 * r, w);
+          if (HL) st16(s_col(x) + lanes + 32 * r + 16, wl);
+        }
+        wait_st();
+        umma::fence_before();
+        arrive(bar(sm.p_full[x]));
+      }
+
+      // ---- the piece's rows
+      if (mine > 0) wait(sm.o_fin[x], pieces_done[x]);
+      umma::fence_after();
+      float f0 = 1.f, f1 = 0.f;
+      if (SPLIT && both) {  // the even set's threads merge the odd one's
+        if (x == 1) {
+          sm.m[row] = M;
+          sm.l[row] = l;
+        }
+        umma::fence_before();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        umma::fence_after();
+        if (x == 0) {
+          const float m1 = sm.m[row], m = fmaxf(M, m1);
+          f0 = exp2f(M - m);
+          f1 = exp2f(m1 - m);
+          l = f0 * l + f1 * sm.l[row];
+          M = m;
+        }
+      }
+      if (x == 0 || (!SPLIT && both)) {
+        const bool done = q.starts && q.ends;
+        float *slot = p.slots + (size_t)(2 * c + (q.starts ? 1 : 0)) * RT * (D + 2);
+        const float inv = 1.0f / (l * a.vq.sqrt_d * sm.scale[1]);
+#pragma unroll
+        for (int r = 0; r < NC; ++r) {
+          uint32_t o[32];
+          float y[32];
+          umma::ld32(o_col(x) + lanes + 32 * r, o);
+          umma::wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]);
+          if (SPLIT && both) {
+            umma::ld32(o_col(1) + lanes + 32 * r, o);
+            umma::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] = y[e] * f0 + __uint_as_float(o[e]) * f1;
+          }
+          if (done) {  // inverse rotation: within the run here, over the runs below
+            dev::fwht_local<32>(y);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(y[e]);
+            st32(o_col(x) + lanes + 32 * r, o);
+          } else if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4 *>(slot + ((size_t)(8 * r + e / 4) * RT + i) * 4) =
+                  make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          }
+        }
+        if (!done && live) {
+          slot[(size_t)D * RT + i] = M;
+          slot[(size_t)(D + 1) * RT + i] = l;
+        }
+        if (done) {
+          wait_st();
+          const bool none = l == 0.f;  // no token seen
+          const int qi = (q.row0 + i) / G;
+          const int64_t orow = (int64_t)(q.q0 + qi) * a.Hq + q.h * G + (q.row0 + i - qi * G);
+          uint16_t *out = static_cast<uint16_t *>(a.out) + orow * D;
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            uint32_t v[NC][8];
+#pragma unroll
+            for (int r = 0; r < NC; ++r) ld8(o_col(x) + lanes + 32 * r + j, v[r]);
+            umma::wait_ld();
+            float y[NC][8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float z[NC];
+#pragma unroll
+              for (int r = 0; r < NC; ++r) z[r] = __uint_as_float(v[r][e]);
+              dev::fwht_local<NC>(z);
+#pragma unroll
+              for (int r = 0; r < NC; ++r) y[r][e] = z[r];
+            }
+            if (live) {
+#pragma unroll
+              for (int r = 0; r < NC; ++r) {
+                const int8_t *sg = a.vq.signs + 32 * r + j;
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float u = none ? 0.f : y[r][2 * e] * inv * (float)__ldg(sg + 2 * e);
+                  const float t = none ? 0.f : y[r][2 * e + 1] * inv * (float)__ldg(sg + 2 * e + 1);
+                  if (a.dtype == TQ_BF16) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(u, t);
+                    w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                  } else {
+                    const __half2 h = __floats2half2_rn(u, t);
+                    w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                  }
+                }
+                *reinterpret_cast<uint4 *>(out + 32 * r + j) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          }
+          if (live && a.lse) a.lse[orow] = none ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
+        }
+      }
+      umma::fence_before();
+    }
+    blocks_done += nblk;
+    if (SPLIT) {
+      items_done[0] += both ? (nblk + 1) / 2 : nblk;
+      items_done[1] += both ? nblk / 2 : 0;
+    } else {
+      items_done[0] += nblk;
+      items_done[1] += both ? nblk : 0;
+    }
+    ++pieces_done[0];
+    pieces_done[1] += both;
+    at += nblk;
+    __syncthreads();
+    umma::fence_after();
+  }
+  if (tid == 0) p.desc[c] = desc;
+  __syncthreads();
+  if (warp == 12) umma::dealloc(tmem, 512);
+}
+
+// Merges the pieces of the unit that starts last in CTA c's range and goes on
+// behind it, in the order of the tokens: 32 rows a block, a warp a row at a time.
+template <int D>
+__global__ void __launch_bounds__(256) paged_tile_merge_kernel(const __grid_constant__ TileParams p) {
+  const PagedAttentionArgs &a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x, RT = p.rt;
+  const float vs = table_scale(a.vq.centroids, lane);
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int4 desc = __ldcg(p.desc + c);
+  if (desc.x == 0) return;
+  const int G = a.Hq / a.Hkv;
+  const Req req = load_req(a, desc.y, p.faults);
+  const int row0 = desc.z * RT, nrows = min(RT, req.n * G - row0);
+  auto slot = [&](int k) { return p.slots + (size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * RT * (D + 2); };
+  for (int i = 32 * blockIdx.y + warp; i < min(nrows, 32 * (int)blockIdx.y + 32); i += 8) {
+    float m = -FLT_MAX;
+    for (int k = lane; k < desc.x; k += 32) m = fmaxf(m, __ldcg(slot(k) + (size_t)D * RT + i));
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(dev::kFull, m, x));
+    float L = 0.f, y[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) y[e] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < desc.x; ++k) {
+      const float *s = slot(k);
+      const float f = exp2f(__ldcg(s + (size_t)D * RT + i) - m);
+      L = fmaf(f, __ldcg(s + (size_t)(D + 1) * RT + i), L);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) {
+        const int d = lane * (D / 32) + e;
+        y[e] = fmaf(f, __ldcg(s + ((size_t)(d >> 2) * RT + i) * 4 + (d & 3)), y[e]);
+      }
+    }
+    const int qi = (row0 + i) / G;
+    store_out<D>(a, (int64_t)req.q0 + qi, desc.w * G + (row0 + i) - qi * G, lane, y, m, L, 1.0f / (a.vq.sqrt_d * vs));
+  }
+}
+
+// Workspace: descriptors, slots, the line, turned rows and their factors.
+struct Layout {
+  size_t slots, first, line, qhi, qlo, qf, end;
+};
+
+Layout layout(int R, int64_t T, int Hq, int Hkv, int d) {
+  const size_t ctas = decode_ctas();
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  Layout l;
+  l.slots = up(ctas * sizeof(int4));
+  l.first = up(l.slots + 2 * ctas * 256 * (d + 2) * sizeof(float));
+  l.line = up(l.first + ((size_t)R + 1) * 4);
+  const size_t tiles = (size_t)T * (Hq / Hkv) / 128 + R + 1;  // at most, in tiles of 128 rows
+  l.qhi = up(l.line + tiles * 8);
+  l.qlo = up(l.qhi + (size_t)T * Hq * d * 2);
+  l.qf = up(l.qlo + (size_t)T * Hq * d * 2);
+  l.end = up(l.qf + (size_t)T * Hq * 4);
+  return l;
+}
+
+template <int D, bool SPLIT, bool HL>
+cudaError_t run_tile(const TileParams &p, cudaStream_t s) {
+  const int ctas = decode_ctas();
+  const int64_t rows = p.a.T * p.a.Hq, rpb = 8 * (512 / D);
+  const int prep = 1 + (int)min((rows + rpb - 1) / rpb, (int64_t)ctas * 8);
+  paged_tile_prep_kernel<D, HL><<<prep, 256, 0, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int dyn = (int)(kHighAddr + 3 * Tile<D>::kBytes) - 1024;
+  e = cudaFuncSetAttribute(paged_tile_kernel<D, SPLIT, HL>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)dyn;
+  e = cudaLaunchKernelEx(&cfg, paged_tile_kernel<D, SPLIT, HL>, p);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(p.rt / 32));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, paged_tile_merge_kernel<D>, p);
+}
+
+template <int D>
+cudaError_t run_d(const TileParams &p, cudaStream_t s) {
+  if (p.a.dtype == TQ_F16) return run_tile<D, true, true>(p, s);
+  return p.rt == 128 ? run_tile<D, true, false>(p, s) : run_tile<D, false, false>(p, s);
+}
+
+}  // namespace
+
+size_t paged_tile_workspace(int R, int64_t T, int Hq, int Hkv, int d) { return layout(R, T, Hq, Hkv, d).end; }
+
+cudaError_t launch_paged_tile(const PagedAttentionArgs &a, cudaStream_t s) {
+  TileParams p{};
+  p.a = a;
+  const cudaError_t e = fault_word(&p.faults);
+  if (e != cudaSuccess) return e;
+  // few rows a unit, or fp16 outputs: the blocks are split over the two sets instead of the rows
+  p.rt = a.dtype == TQ_F16 || (int64_t)a.max_q * (a.Hq / a.Hkv) <= 128 ? 128 : 256;
+  const Layout l = layout(a.R, a.T, a.Hq, a.Hkv, a.kq.d);
+  char *w = static_cast<char *>(a.ws);
+  p.desc = reinterpret_cast<int4 *>(w);
+  p.slots = reinterpret_cast<float *>(w + l.slots);
+  p.first = reinterpret_cast<int32_t *>(w + l.first);
+  p.line = reinterpret_cast<int64_t *>(w + l.line);
+  p.qhi = reinterpret_cast<const __half *>(w + l.qhi);
+  p.qlo = reinterpret_cast<const __half *>(w + l.qlo);
+  p.qf = reinterpret_cast<const float *>(w + l.qf);
+  return a.kq.d == 64 ? run_d<64>(p, s) : run_d<128>(p, s);
+}
+
+}  // namespace tq
