@@ -509,36 +509,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
       const int32_t *row = a.table + (int64_t)q.r * a.table_stride;
       uint4 kc[IT], vc[IT];
       float kn = 0.f, vn = 0.f;  // of token 32 wq + lane
-      bool have = false;
-      auto record = [&](int j, int64_t &kr, int64_t &vr) {
-        kr = vr = -1;
-        if (j >= q.first && j < q.kv) {
-          const int page = j / a.page_size, off = j - page * a.page_size;
-          const int id = __ldg(row + page);
-          if ((unsigned)id < (unsigned)a.n_pages) {
-            kr = id * a.k.sb + q.h * a.k.sh + off * a.k.sn;
-            vr = id * a.v.sb + q.h * a.v.sh + off * a.v.sn;
-          } else {
-            atomicOr(p.faults, kFaultIndex);
-          }
-        }
+      // page of token 32 wq + lane of block b (-1: none is needed), and its record
+      auto page_id = [&](int b) {
+        const int j = b * kBlk + 32 * wq + lane;
+        return b < q.b1 && j >= q.first && j < q.kv ? __ldg(row + j / a.page_size) : -1;
       };
-      auto load = [&](int b) {
-        // the record of token 32 wq + lane; the lanes' tokens of each pass come from there
-        int64_t kr, vr;
-        record(b * kBlk + 32 * wq + lane, kr, vr);
-        have = kr >= 0;
-        kn = have ? __ldg(a.k.norms + kr) : 0.f;
-        vn = have ? __ldg(a.v.norms + vr) : 0.f;
+      auto record = [&](int b, int id, int64_t &kr, int64_t &vr) {
+        const int j = b * kBlk + 32 * wq + lane, off = j % a.page_size;
+        const bool want = b < q.b1 && j >= q.first && j < q.kv;
+        const bool ok = want && (unsigned)id < (unsigned)a.n_pages;
+        if (want && !ok) atomicOr(p.faults, kFaultIndex);
+        kr = ok ? id * a.k.sb + q.h * a.k.sh + off * a.k.sn : -1;
+        vr = ok ? id * a.v.sb + q.h * a.v.sh + off * a.v.sn : -1;
+      };
+      // 16 code bytes of the lane's token of each pass; the record comes from the lane that has it
+      auto load = [&](const uint8_t *codes, int64_t rec, uint4 (&x)[IT]) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-          const int64_t k1 = __shfl_sync(dev::kFull, kr, TPI * i + tk), v1 = __shfl_sync(dev::kFull, vr, TPI * i + tk);
-          kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
-          if (k1 >= 0) {
-            kc[i] = __ldg(reinterpret_cast<const uint4 *>(a.k.codes + k1 * (D / 2)) + ch);
-            vc[i] = __ldg(reinterpret_cast<const uint4 *>(a.v.codes + v1 * (D / 2)) + ch);
-          }
+          const int64_t r1 = __shfl_sync(dev::kFull, rec, TPI * i + tk);
+          x[i] = r1 >= 0 ? __ldg(reinterpret_cast<const uint4 *>(codes + r1 * (D / 2)) + ch) : make_uint4(0, 0, 0, 0);
         }
+      };
+      auto load_norms = [&](int64_t kr, int64_t vr) {
+        kn = kr >= 0 ? __ldg(a.k.norms + kr) : 0.f;
+        vn = kr >= 0 ? __ldg(a.v.norms + vr) : 0.f;
       };
       auto decode = [&](uint32_t tile, uint32_t tab, const uint4 (&x)[IT]) {
 #pragma unroll
@@ -546,15 +540,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
           const int t = 32 * wq + TPI * i + tk;
           const uint32_t to = tile + (t >> 3) * GB + ch * 4 * 128 + (t & 7) * 16;
           const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t v[4][4];  // all reads first: a write in between would hold the next ones back
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            sts128(to + 128 * j, pair<0>(w[j], tab), pair<1>(w[j], tab), pair<2>(w[j], tab), pair<3>(w[j], tab));
+          for (int j = 0; j < 4; ++j) {
+            v[j][0] = pair<0>(w[j], tab);
+            v[j][1] = pair<1>(w[j], tab);
+            v[j][2] = pair<2>(w[j], tab);
+            v[j][3] = pair<3>(w[j], tab);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sts128(to + 128 * j, v[j][0], v[j][1], v[j][2], v[j][3]);
         }
       };
-      load(q.b0);
+      // a block's page numbers are read two blocks ahead, its codes and norms one block ahead
+      int64_t kr, vr;
+      record(q.b0, page_id(q.b0), kr, vr);
+      load(a.k.codes, kr, kc);
+      load(a.v.codes, vr, vc);
+      load_norms(kr, vr);
+      bool have = kr >= 0;
+      record(q.b0 + 1, page_id(q.b0 + 1), kr, vr);
       for (int b = 0; b < nblk; ++b) {
         const uint32_t u = blocks_done + b;
         const int nb = u & 1;
+        const int id2 = page_id(q.b0 + b + 2);
         // free: the products of the buffer's last block, u - 2, were done before V of block u - 1 was written
         sm.kn[nb][32 * wq + lane] = kn;
         sm.vn[nb][32 * wq + lane] = vn;
@@ -566,11 +575,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         decode(kK, ktab, kc);
         umma::fence_async_smem();
         arrive(bar(sm.k_full));
+        load(a.k.codes, kr, kc);
+        load_norms(kr, vr);
+        have = kr >= 0;
         if (u > 0) wait(sm.v_free, u - 1);
         decode(kV, vtab, vc);
         umma::fence_async_smem();
         arrive(bar(sm.v_full));
-        if (b + 1 < nblk) load(q.b0 + b + 1);
+        load(a.v.codes, vr, vc);
+        record(q.b0 + b + 2, id2, kr, vr);
       }
     } else {
       // ================= softmax: set x, a row a thread
@@ -597,45 +610,84 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         const uint4 vm = *reinterpret_cast<const uint4 *>(sm.valid[nb]);
         const uint32_t valid[4] = {vm.x, vm.y, vm.z, vm.w};
         const bool whole = see_lo <= j0 && see_hi >= j0 + kBlk && (vm.x & vm.y & vm.z & vm.w) == ~0u;
-        const bool edge = !__all_sync(dev::kFull, whole);
-        auto mask = [&](int r) {  // tokens of run r that the row sees
+        const float *kns = sm.kn[nb], *vns = sm.vn[nb], *lvs = sm.lv[nb];
+        auto mask = [&](int r) {  // tokens of run r (32 columns) that the row sees
           const int lo = max(see_lo - j0 - 32 * r, 0), hi = min(see_hi - j0 - 32 * r, 32);
           const uint32_t m = hi <= 0 || lo >= 32 ? 0u : (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
           return m & valid[r];
         };
-        // the largest logit + log2 ||v||, relative to `ref`
-        auto top = [&](float ref) {
-          float mx = -INFINITY;
+        // the largest logit + log2 ||v|| of the row
+        auto top = [&](auto edge) {
+          constexpr bool EDGE = decltype(edge)::value;
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             uint32_t s[32];
             umma::ld32(s_col(x) + lanes + 32 * r, s);
             umma::wait_ld();
-            const uint32_t m = edge ? mask(r) : ~0u;
+            const uint32_t m = EDGE ? mask(r) : ~0u;
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 kn = *reinterpret_cast<const float4 *>(&sm.kn[nb][32 * r + e]);
-              const float4 lv = *reinterpret_cast<const float4 *>(&sm.lv[nb][32 * r + e]);
-              const float t0 = fmaf(__uint_as_float(s[e]), kn.x * f, lv.x - ref);
-              const float t1 = fmaf(__uint_as_float(s[e + 1]), kn.y * f, lv.y - ref);
-              const float t2 = fmaf(__uint_as_float(s[e + 2]), kn.z * f, lv.z - ref);
-              const float t3 = fmaf(__uint_as_float(s[e + 3]), kn.w * f, lv.w - ref);
-              if (edge) {
-                if (m >> e & 1) mx = fmaxf(mx, t0);
-                if (m >> (e + 1) & 1) mx = fmaxf(mx, t1);
-                if (m >> (e + 2) & 1) mx = fmaxf(mx, t2);
-                if (m >> (e + 3) & 1) mx = fmaxf(mx, t3);
-              } else {
-                mx = fmaxf(mx, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)));
+              const float4 kn = *reinterpret_cast<const float4 *>(kns + 32 * r + e);
+              const float4 lv = *reinterpret_cast<const float4 *>(lvs + 32 * r + e);
+              float k0, k1, k2, k3, t[4];
+              dev::mul_x2(k0, k1, kn.x, kn.y, f, f);
+              dev::mul_x2(k2, k3, kn.z, kn.w, f, f);
+              dev::fma_x2(t[0], t[1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), k0, k1, lv.x, lv.y);
+              dev::fma_x2(t[2], t[3], __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]), k2, k3, lv.z, lv.w);
+#pragma unroll
+              for (int o = 0; o < 4; ++o)
+                if (!EDGE || (m >> (e + o) & 1)) mx[o] = fmaxf(mx[o], t[o]);
+            }
+          }
+          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        };
+        // Weights relative to M, of run r: their sum, and times ||v|| as operand words (hi, and with HL lo).
+        auto weights = [&](auto edge, int r, float &sum, uint32_t *w, uint32_t *wl) {
+          constexpr bool EDGE = decltype(edge)::value;
+          uint32_t s[32];
+          umma::ld32(s_col(x) + lanes + 32 * r, s);
+          umma::wait_ld();
+          const uint32_t m = EDGE ? mask(r) : ~0u;
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 kn = *reinterpret_cast<const float4 *>(kns + 32 * r + e);
+            const float4 vn = *reinterpret_cast<const float4 *>(vns + 32 * r + e);
+            float k0, k1, k2, k3, t[4];
+            dev::mul_x2(k0, k1, kn.x, kn.y, f, f);
+            dev::mul_x2(k2, k3, kn.z, kn.w, f, f);
+            dev::fma_x2(t[0], t[1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), k0, k1, -M, -M);
+            dev::fma_x2(t[2], t[3], __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]), k2, k3, -M, -M);
+#pragma unroll
+            for (int o = 0; o < 4; ++o) {
+              t[o] = exp2_approx(t[o]);
+              if (EDGE) t[o] = m >> (e + o) & 1 ? t[o] : 0.f;
+            }
+            dev::add_x2(l0, l1, l0, l1, t[0], t[1]);
+            dev::add_x2(l0, l1, l0, l1, t[2], t[3]);
+            dev::mul_x2(t[0], t[1], t[0], t[1], vn.x, vn.y);
+            dev::mul_x2(t[2], t[3], t[2], t[3], vn.z, vn.w);
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              if (EDGE) {  // a masked token's norm may be anything
+                t[2 * o] = m >> (e + 2 * o) & 1 ? t[2 * o] : 0.f;
+                t[2 * o + 1] = m >> (e + 2 * o + 1) & 1 ? t[2 * o + 1] : 0.f;
+              }
+              const __half2 h = __floats2half2_rn(t[2 * o], t[2 * o + 1]);
+              w[e / 2 + o] = *reinterpret_cast<const uint32_t *>(&h);
+              if (HL) {
+                const float2 back = __half22float2(h);
+                const __half2 lo = __floats2half2_rn(t[2 * o] - back.x, t[2 * o + 1] - back.y);
+                wl[e / 2 + o] = *reinterpret_cast<const uint32_t *>(&lo);
               }
             }
           }
-          return mx;
+          sum += l0 + l1;
         };
-        // M is a reference that moves only when a weight times its norm would pass 2^8
-        const float rel = k == 0 ? INFINITY : top(M);
-        if (__any_sync(dev::kFull, rel > 8.f)) {
-          const float m2 = fmaxf(M, top(0.f)), r2 = exp2f(M - m2);
+        // moves the reference M to the block's largest value if that is above it
+        auto move = [&](float mx) {
+          const float m2 = fmaxf(M, mx), r2 = exp2f(M - m2);
           M = m2;
           l *= r2;
           if (k > 0) {  // the scores' barrier says that the products before them are done, those into O too
@@ -649,41 +701,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
               st32(o_col(x) + lanes + 32 * r, o);
             }
           }
-        }
+        };
+        // M moves only when a weight times its norm would pass 2^8
+        auto item = [&](auto edge) {
+          const float mx = top(edge);
+          if (__any_sync(dev::kFull, mx > M + 8.f)) move(mx);
+          float sum = 0.f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          uint32_t s[32], w[16], wl[16];
-          umma::ld32(s_col(x) + lanes + 32 * r, s);
-          umma::wait_ld();
-          const uint32_t m = edge ? mask(r) : ~0u;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 kn = *reinterpret_cast<const float4 *>(&sm.kn[nb][32 * r + e]);
-            const float4 vn = *reinterpret_cast<const float4 *>(&sm.vn[nb][32 * r + e]);
-            const float kk[4] = {kn.x, kn.y, kn.z, kn.w}, vv[4] = {vn.x, vn.y, vn.z, vn.w};
-            float t[4];
-#pragma unroll
-            for (int o = 0; o < 4; ++o) {
-              t[o] = exp2_approx(fmaf(__uint_as_float(s[e + o]), kk[o] * f, -M));
-              if (edge && !(m >> (e + o) & 1)) t[o] = 0.f;
-            }
-            l += (t[0] + t[1]) + (t[2] + t[3]);
-#pragma unroll
-            for (int o = 0; o < 4; ++o) t[o] = edge && !(m >> (e + o) & 1) ? 0.f : t[o] * vv[o];
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              const __half2 h = __floats2half2_rn(t[2 * o], t[2 * o + 1]);
-              w[e / 2 + o] = *reinterpret_cast<const uint32_t *>(&h);
-              if (HL) {
-                const float2 back = __half22float2(h);
-                const __half2 lo = __floats2half2_rn(t[2 * o] - back.x, t[2 * o + 1] - back.y);
-                wl[e / 2 + o] = *reinterpret_cast<const uint32_t *>(&lo);
-              }
-            }
+          for (int r = 0; r < 4; ++r) {
+            uint32_t w[16], wl[16];
+            weights(edge, r, sum, w, wl);
+            st16(s_col(x) + lanes + 32 * r, w);
+            if (HL) st16(s_col(x) + lanes + 32 * r + 16, wl);
           }
-          st16(s_col(x) + lanes + 32 * r, w);
-          if (HL) st16(s_col(x) + lanes + 32 * r + 16, wl);
-        }
+          l += sum;
+        };
+        if (__all_sync(dev::kFull, whole)) item(std::false_type{});
+        else item(std::true_type{});
         wait_st();
         umma::fence_before();
         arrive(bar(sm.p_full[x]));
