@@ -7,17 +7,18 @@
 // the order of the tokens.
 //
 // Per block, on the fifth-generation tensor cores: S = Q K^T and O += P V with
-// fp16 operands and fp32 sums in tensor memory.  Roles of a CTA's 13 warps:
-//   * 4 warps decode: a token's 64 code bytes become 128 fp16 centroids in the
-//     operand tile, a code byte (two codes) being one read of a table of
-//     centroid pairs, one copy per lane, whose address is one byte permute.
-//     K and V tiles have the same layout, a token's 8 coordinates a 16-byte
-//     row: K-major for the scores, and for the values, whose sum runs over
-//     tokens, the transposed operand form.  No V transpose is ever made.
+// fp16 operands and fp32 sums in tensor memory.  Roles of a CTA's 16 warps:
+//   * 4 warps decode K and 4 V: a token's 64 code bytes become 128 fp16
+//     centroids in the operand tile, a code byte (two codes) being one read of
+//     a table of centroid pairs, one copy per lane, whose address is one byte
+//     permute.  Both tiles have the same layout, a token's 8 coordinates a
+//     16-byte row: K-major for the scores, and for the values, whose sum runs
+//     over tokens, the transposed operand form.  No V transpose is ever made.
 //   * 2 x 4 warps softmax, a query row a thread: scores from tensor memory
 //     times ||k||, the running reference and sum, weights times ||v|| back
-//     into tensor memory as the next product's operand.
-//   * 1 thread issues the products.
+//     into tensor memory as the next product's operand.  One thread of each
+//     set issues the set's products: the values' of a block, then the scores
+//     of its next one, which take the weights' place behind them.
 // Two sets of rows (or of blocks) alternate, so that one's products run while
 // the other's softmax does:
 //   wide:  256 rows a tile, both halves against every block (bf16 outputs;
@@ -41,7 +42,7 @@ namespace {
 using namespace paged;
 
 constexpr int kBlk = 128;                 // tokens per block
-constexpr int kThreads = 416;             // 2 x 4 softmax warps, 4 decode warps, 1 for the products
+constexpr int kThreads = 512;             // 2 x 4 softmax warps, 4 warps decode K and 4 V
 constexpr uint32_t kTabAddr = 0x10000u;   // the pair tables: 64 KiB at this shared address
 constexpr uint32_t kHighAddr = 0x20000u;  // V, K and the second query tile
 
@@ -223,14 +224,18 @@ struct Piece {
   int starts, ends;  // whether they hold the unit's first and last block
 };
 
+constexpr int kNormBufs = 4;
+
 struct Low {
-  uint64_t k_full, k_free, v_full, v_free, n_full[2], s_full[2], p_full[2], o_fin[2];
+  // A tile's blocks alternate between two barriers: with split blocks a set waits for every other one only.
+  uint64_t k_full[2], v_full[2], k_free, v_free, n_full[kNormBufs], s_full[2], o_fin[2];
   uint32_t tmem, pad;
   Piece piece;
-  alignas(16) float kn[2][kBlk], vn[2][kBlk], lv[2][kBlk];  // of a block's tokens: ||k||, ||v||, max(log2 ||v||, -64)
-  alignas(16) uint32_t valid[2][kBlk / 32];     // tokens with a record
-  float f[256];                                 // score factors of the rows
-  float m[128], l[128];                         // the odd set's references and sums (split)
+  // of a block's tokens: ||k||, ||v||, max(log2 ||v||, -64), and whether they have a record
+  alignas(16) float kn[kNormBufs][kBlk], vn[kNormBufs][kBlk], lv[kNormBufs][kBlk];
+  alignas(16) uint32_t valid[kNormBufs][kBlk / 32];
+  float f[256];          // score factors of the rows
+  float m[128], l[128];  // the odd set's references and sums (split)
   float scale[2];
 };
 
@@ -318,15 +323,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
       pairs[warp * 256 + e] = *reinterpret_cast<const uint32_t *>(&h);
     }
   }
-  if (warp == 12) umma::alloc(&sm.tmem, 512);
+  if (warp == 15) umma::alloc(&sm.tmem, 512);
   if (tid == 0) {
-    umma::mbar_init(bar(sm.k_full), 128);
-    umma::mbar_init(bar(sm.v_full), 128);
-    umma::mbar_init(bar(sm.k_free), 1);
-    umma::mbar_init(bar(sm.v_free), 1);
+    umma::mbar_init(bar(sm.k_free), 2);
+    umma::mbar_init(bar(sm.v_free), 2);
+    for (int x = 0; x < kNormBufs; ++x) umma::mbar_init(bar(sm.n_full[x]), 256);
     for (int x = 0; x < 2; ++x) {
-      umma::mbar_init(bar(sm.n_full[x]), 128);
-      umma::mbar_init(bar(sm.p_full[x]), 128);
+      umma::mbar_init(bar(sm.k_full[x]), 128);
+      umma::mbar_init(bar(sm.v_full[x]), 128);
       umma::mbar_init(bar(sm.s_full[x]), 1);
       umma::mbar_init(bar(sm.o_fin[x]), 1);
     }
@@ -364,7 +368,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
 
   int r = -1, h = 0, tile = 0, ta = 0, tb = 0;  // the unit (thread 0)
   Req req{};
-  while (at < end) {
+  Piece q;
+  int nblk = 0;
+  bool both = false;  // whether both sets have work
+  // The next piece of the range, its query rows in the operand tiles: all threads together.
+  auto next_piece = [&]() -> bool {
+    if (nblk > 0) {
+      blocks_done += nblk;
+      items_done[0] += SPLIT && both ? (nblk + 1) / 2 : nblk;
+      items_done[1] += !both ? 0 : SPLIT ? nblk / 2 : nblk;
+      ++pieces_done[0];
+      pieces_done[1] += both;
+      at += nblk;
+      umma::fence_before();
+      __syncthreads();
+      umma::fence_after();
+    }
+    if (at >= end) return false;
     // ---- the piece: one thread finds the first and walks on from unit to unit
     if (tid == 0) {
       int skip = 0;  // blocks of the unit in front of the range
@@ -425,8 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
       }
     }
     __syncthreads();
-    const Piece q = sm.piece;
-    const int nblk = q.b1 - q.b0;
+    q = sm.piece;
+    nblk = q.b1 - q.b0;
+    both = SPLIT ? nblk > 1 : q.nrows > 128;
     // ---- query rows into the operand tiles: 16-byte words of 8 coordinates
     for (int i = tid; i < RT * (D / 8); i += kThreads) {
       const int row = i / D * 8 + (i & 7), w = (i >> 3) % (D / 8);
@@ -447,98 +468,74 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
     umma::fence_async_smem();
     __syncthreads();
 
-    // sets at work, items of each; item k of the piece: block k / 2 (wide, both sets) or k (split)
-    const bool both = SPLIT ? nblk > 1 : q.nrows > 128;
-    const int items = SPLIT || !both ? nblk : 2 * nblk;
-    auto set_of = [&](int k) { return both ? k & 1 : 0; };
-    auto blk_of = [&](int k) { return SPLIT || !both ? k : k >> 1; };
+    return true;
+  };
 
-    if (warp == 12) {
-      // ================= products
-      if (lane == 0) {
-        uint32_t n_x[2] = {items_done[0], items_done[1]};
-        auto scores = [&](int k) {
-          const int x = set_of(k), b = blk_of(k);
-          if (SPLIT || !both || x == 0) wait(sm.k_full, blocks_done + b);
-          umma::fence_after();
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            const uint64_t kd = umma::desc(kK + s * 256, 128, GB);
-            if (HL) {
-              umma::mma_f16(s_col(x), umma::desc(kQ0 + s * 256, 128, GB), kd, kIdS, s > 0);
-              umma::mma_f16(s_col(x), umma::desc(kQ1 + s * 256, 128, GB), kd, kIdS, 1);
-            } else {
-              umma::mma_f16(s_col(x), umma::desc((SPLIT || x == 0 ? kQ0 : kQ1) + s * 256, 128, GB), kd, kIdS, s > 0);
-            }
-          }
-          umma::commit(bar(sm.s_full[x]));
-          if (SPLIT || !both || x == 1) umma::commit(bar(sm.k_free));
-        };
-        scores(0);
-        if (both) scores(1);
-        for (int k = 0; k < items; ++k) {
-          const int x = set_of(k), b = blk_of(k);
-          if (SPLIT || !both || x == 0) wait(sm.v_full, blocks_done + b);
-          wait(sm.p_full[x], n_x[x]);
-          umma::fence_after();
-          const bool first = k < (both ? 2 : 1);
-#pragma unroll
-          for (int s = 0; s < kBlk / 16; ++s) {
-            const uint64_t vd = umma::desc(kV + s * 2 * GB, GB, 128);
-            const uint32_t pc = s_col(x) + 32 * (s >> 1) + 8 * (s & 1);
-            mma_ts(o_col(x), pc, vd, kIdO, !first || s > 0);
-            if (HL) mma_ts(o_col(x), pc + 16, vd, kIdO, 1);
-          }
-          if (SPLIT || !both || x == 1) umma::commit(bar(sm.v_free));
-          if (k + (both ? 2 : 1) >= items) umma::commit(bar(sm.o_fin[x]));
-          ++n_x[x];
-          // the set's next scores go where its weights were: behind their product
-          const int next = k + (both ? 2 : 1);
-          if (next < items) scores(next);
-        }
-      }
-      __syncwarp();
-    } else if (warp >= 8) {
-      // ================= codes to operands: 32 tokens of a block a warp, a 16-byte word of each a lane
-      constexpr int TPI = D == 128 ? 8 : 16;   // tokens per pass
-      constexpr int IT = 32 / TPI;
-      const int wq = warp - 8, tk = lane % TPI, ch = lane / TPI;
-      uint32_t ktab, vtab;
-      asm("mov.b32 %0, %1;" : "=r"(ktab) : "r"(kTabAddr + 4 * lane));
-      asm("mov.b32 %0, %1;" : "=r"(vtab) : "r"(kTabAddr + 4 * lane + 128));
+  if (warp >= 8) {
+    // ================= codes to operands: K by warps 8..11, V by 12..15, 32 tokens of a block a warp, a 16-byte
+    // word of each a lane
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    const bool is_k = warp < 12;
+    constexpr int TPI = D == 128 ? 8 : 16;  // tokens per pass
+    constexpr int IT = 32 / TPI;
+    const int wq = warp & 3, tk = lane % TPI, ch = lane / TPI;
+    uint32_t tab;
+    asm("mov.b32 %0, %1;" : "=r"(tab) : "r"(kTabAddr + 4 * lane + (is_k ? 0 : 128)));
+    const uint32_t tile_at = is_k ? kK : kV;
+    const CacheView cv = is_k ? a.k : a.v;
+    while (next_piece()) {
       const int32_t *row = a.table + (int64_t)q.r * a.table_stride;
-      uint4 kc[IT], vc[IT];
-      float kn = 0.f, vn = 0.f;  // of token 32 wq + lane
-      // page of token 32 wq + lane of block b (-1: none is needed), and its record
+      // page of token 32 wq + lane of block b (none is needed: -1), and its record
       auto page_id = [&](int b) {
         const int j = b * kBlk + 32 * wq + lane;
         return b < q.b1 && j >= q.first && j < q.kv ? __ldg(row + j / a.page_size) : -1;
       };
-      auto record = [&](int b, int id, int64_t &kr, int64_t &vr) {
+      auto record = [&](int b, int id) -> int64_t {
         const int j = b * kBlk + 32 * wq + lane, off = j % a.page_size;
-        const bool want = b < q.b1 && j >= q.first && j < q.kv;
-        const bool ok = want && (unsigned)id < (unsigned)a.n_pages;
-        if (want && !ok) atomicOr(p.faults, kFaultIndex);
-        kr = ok ? id * a.k.sb + q.h * a.k.sh + off * a.k.sn : -1;
-        vr = ok ? id * a.v.sb + q.h * a.v.sh + off * a.v.sn : -1;
+        if (b >= q.b1 || j < q.first || j >= q.kv) return -1;
+        if ((unsigned)id >= (unsigned)a.n_pages) {
+          atomicOr(p.faults, kFaultIndex);
+          return -1;
+        }
+        return id * cv.sb + q.h * cv.sh + off * cv.sn;
       };
-      // 16 code bytes of the lane's token of each pass; the record comes from the lane that has it
-      auto load = [&](const uint8_t *codes, int64_t rec, uint4 (&x)[IT]) {
+      uint4 x[IT];
+      float norm;
+      // 16 code bytes of the lane's token of each pass (the record comes from the lane that has it), and the norm
+      // of token 32 wq + lane
+      auto load = [&](int64_t rec) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           const int64_t r1 = __shfl_sync(dev::kFull, rec, TPI * i + tk);
-          x[i] = r1 >= 0 ? __ldg(reinterpret_cast<const uint4 *>(codes + r1 * (D / 2)) + ch) : make_uint4(0, 0, 0, 0);
+          x[i] = r1 >= 0 ? __ldg(reinterpret_cast<const uint4 *>(cv.codes + r1 * (D / 2)) + ch) : make_uint4(0, 0, 0, 0);
         }
+        norm = rec >= 0 ? __ldg(cv.norms + rec) : 0.f;
       };
-      auto load_norms = [&](int64_t kr, int64_t vr) {
-        kn = kr >= 0 ? __ldg(a.k.norms + kr) : 0.f;
-        vn = kr >= 0 ? __ldg(a.v.norms + vr) : 0.f;
-      };
-      auto decode = [&](uint32_t tile, uint32_t tab, const uint4 (&x)[IT]) {
+      // a block's page numbers are read two blocks ahead, its codes and norms one block ahead
+      int64_t rec = record(q.b0, page_id(q.b0));
+      load(rec);
+      bool have = rec >= 0;
+      rec = record(q.b0 + 1, page_id(q.b0 + 1));
+      for (int b = 0; b < nblk; ++b) {
+        const uint32_t u = blocks_done + b;
+        const int nb = u % kNormBufs;
+        const int id2 = page_id(q.b0 + b + 2);
+        // Free: the buffer was block u - 4's.  This thread has seen the scores of block u - 2 done (or its
+        // values), which were issued behind the products with the weights of block u - 4 (or u - 3 and u - 4).
+        if (is_k) {
+          sm.kn[nb][32 * wq + lane] = norm;
+          const unsigned ok = __ballot_sync(dev::kFull, have);
+          if (lane == 0) sm.valid[nb][wq] = ok;
+        } else {
+          sm.vn[nb][32 * wq + lane] = norm;
+          sm.lv[nb][32 * wq + lane] = fmaxf(log2_approx(norm), -64.f);
+        }
+        arrive(bar(sm.n_full[nb]));
+        if (u > 0) wait(is_k ? sm.k_free : sm.v_free, u - 1);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           const int t = 32 * wq + TPI * i + tk;
-          const uint32_t to = tile + (t >> 3) * GB + ch * 4 * 128 + (t & 7) * 16;
+          const uint32_t to = tile_at + (t >> 3) * GB + ch * 4 * 128 + (t & 7) * 16;
           const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
           uint32_t v[4][4];  // all reads first: a write in between would hold the next ones back
 #pragma unroll
@@ -551,42 +548,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
 #pragma unroll
           for (int j = 0; j < 4; ++j) sts128(to + 128 * j, v[j][0], v[j][1], v[j][2], v[j][3]);
         }
-      };
-      // a block's page numbers are read two blocks ahead, its codes and norms one block ahead
-      int64_t kr, vr;
-      record(q.b0, page_id(q.b0), kr, vr);
-      load(a.k.codes, kr, kc);
-      load(a.v.codes, vr, vc);
-      load_norms(kr, vr);
-      bool have = kr >= 0;
-      record(q.b0 + 1, page_id(q.b0 + 1), kr, vr);
-      for (int b = 0; b < nblk; ++b) {
-        const uint32_t u = blocks_done + b;
-        const int nb = u & 1;
-        const int id2 = page_id(q.b0 + b + 2);
-        // free: the products of the buffer's last block, u - 2, were done before V of block u - 1 was written
-        sm.kn[nb][32 * wq + lane] = kn;
-        sm.vn[nb][32 * wq + lane] = vn;
-        sm.lv[nb][32 * wq + lane] = fmaxf(log2_approx(vn), -64.f);
-        const unsigned ok = __ballot_sync(dev::kFull, have);
-        if (lane == 0) sm.valid[nb][wq] = ok;
-        arrive(bar(sm.n_full[nb]));
-        if (u > 0) wait(sm.k_free, u - 1);
-        decode(kK, ktab, kc);
         umma::fence_async_smem();
-        arrive(bar(sm.k_full));
-        load(a.k.codes, kr, kc);
-        load_norms(kr, vr);
-        have = kr >= 0;
-        if (u > 0) wait(sm.v_free, u - 1);
-        decode(kV, vtab, vc);
-        umma::fence_async_smem();
-        arrive(bar(sm.v_full));
-        load(a.v.codes, vr, vc);
-        record(q.b0 + b + 2, id2, kr, vr);
+        arrive(bar(is_k ? sm.k_full[u & 1] : sm.v_full[u & 1]));
+        load(rec);
+        have = rec >= 0;
+        rec = record(q.b0 + b + 2, id2);
       }
-    } else {
-      // ================= softmax: set x, a row a thread
+    }
+  } else {
+    // ================= softmax: set x, a row a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    while (next_piece()) {
       const int x = warp >> 2, row = (warp & 3) * 32 + lane;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const int i = SPLIT ? row : 128 * x + row;  // row of the tile
@@ -599,12 +571,53 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
       }
       const float f = sm.f[i];
       float M = -FLT_MAX, l = 0.f;
-      const int mine = x < (both ? 2 : 1) ? (SPLIT ? (both ? (nblk + 1 - x) / 2 : nblk) : nblk) : 0;
-      for (int k = 0; k < mine; ++k) {
-        const int b = SPLIT && both ? 2 * k + x : k;
+      // One thread issues the set's products.  The barriers that free a block's tiles take two arrivals: one a set,
+      // or two of the only one that has the block.
+      const bool issuer = (warp & 3) == 0 && lane == 0;
+      auto free_tile = [&](const uint64_t &b) {
+        umma::commit(bar(b));
+        if (SPLIT || !both) umma::commit(bar(b));
+      };
+      auto block = [&](int k) { return SPLIT && both ? 2 * k + x : k; };  // of the set's item k
+      auto scores = [&](int b) {
         const uint32_t u = blocks_done + b;
-        const int nb = u & 1, j0 = (q.b0 + b) * kBlk;
-        wait(sm.n_full[nb], u >> 1);
+        wait(sm.k_full[u & 1], u >> 1);
+        umma::fence_after();
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint64_t kd = umma::desc(kK + s * 256, 128, GB);
+          if (HL) {
+            umma::mma_f16(s_col(x), umma::desc(kQ0 + s * 256, 128, GB), kd, kIdS, s > 0);
+            umma::mma_f16(s_col(x), umma::desc(kQ1 + s * 256, 128, GB), kd, kIdS, 1);
+          } else {
+            umma::mma_f16(s_col(x), umma::desc((SPLIT || x == 0 ? kQ0 : kQ1) + s * 256, 128, GB), kd, kIdS, s > 0);
+          }
+        }
+        umma::commit(bar(sm.s_full[x]));
+        free_tile(sm.k_free);
+      };
+      auto values = [&](int b, bool first, bool last) {
+        const uint32_t u = blocks_done + b;
+        wait(sm.v_full[u & 1], u >> 1);
+        umma::fence_after();
+#pragma unroll
+        for (int s = 0; s < kBlk / 16; ++s) {
+          const uint64_t vd = umma::desc(kV + s * 2 * GB, GB, 128);
+          const uint32_t pc = s_col(x) + 32 * (s >> 1) + 8 * (s & 1);
+          mma_ts(o_col(x), pc, vd, kIdO, !first || s > 0);
+          if (HL) mma_ts(o_col(x), pc + 16, vd, kIdO, 1);
+        }
+        free_tile(sm.v_free);
+        if (last) umma::commit(bar(sm.o_fin[x]));
+      };
+      const int mine = x < (both ? 2 : 1) ? (SPLIT ? (both ? (nblk + 1 - x) / 2 : nblk) : nblk) : 0;
+      if (mine > 0 && issuer) scores(block(0));
+      __syncwarp();
+      for (int k = 0; k < mine; ++k) {
+        const int b = block(k);
+        const uint32_t u = blocks_done + b;
+        const int nb = u % kNormBufs, j0 = (q.b0 + b) * kBlk;
+        wait(sm.n_full[nb], u / kNormBufs);
         wait(sm.s_full[x], items_done[x] + k);
         umma::fence_after();
         const uint4 vm = *reinterpret_cast<const uint4 *>(sm.valid[nb]);
@@ -702,17 +715,40 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
             }
           }
         };
-        // M moves only when a weight times its norm would pass 2^8
+        // M moves only when a weight times its norm would pass 2^8: with HL that is looked for before the
+        // weights, which take the scores' place at once; else the weights are kept in registers, and where one
+        // is too large they are made again
         auto item = [&](auto edge) {
-          const float mx = top(edge);
-          if (__any_sync(dev::kFull, mx > M + 8.f)) move(mx);
           float sum = 0.f;
+          if constexpr (HL) {
+            const float mx = top(edge);
+            if (__any_sync(dev::kFull, mx > M + 8.f)) move(mx);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            uint32_t w[16], wl[16];
-            weights(edge, r, sum, w, wl);
-            st16(s_col(x) + lanes + 32 * r, w);
-            if (HL) st16(s_col(x) + lanes + 32 * r + 16, wl);
+            for (int r = 0; r < 4; ++r) {
+              uint32_t w[16], wl[16];
+              weights(edge, r, sum, w, wl);
+              st16(s_col(x) + lanes + 32 * r, w);
+              st16(s_col(x) + lanes + 32 * r + 16, wl);
+            }
+          } else {
+            uint32_t w[4][16];
+            bool again = k == 0;
+            for (;;) {
+              if (again) move(top(edge));
+              sum = 0.f;
+              __half2 most = __float2half2_rn(0.f);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                weights(edge, r, sum, w[r], nullptr);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) most = __hmax2(most, *reinterpret_cast<const __half2 *>(&w[r][e]));
+              }
+              // a reference that has just moved bounds the weights by 1 (and rounding)
+              if (again || !__any_sync(dev::kFull, __hgt(__hmax(__low2half(most), __high2half(most)), __float2half(256.f)))) break;
+              again = true;
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) st16(s_col(x) + lanes + 32 * r, w[r]);
           }
           l += sum;
         };
@@ -720,7 +756,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         else item(std::true_type{});
         wait_st();
         umma::fence_before();
-        arrive(bar(sm.p_full[x]));
+        // every row's weights are in place: the products with them, and the set's next scores behind those
+        if (x == 0) asm volatile("bar.sync 2, 128;" ::: "memory");
+        else asm volatile("bar.sync 3, 128;" ::: "memory");
+        if (issuer) {
+          umma::fence_after();
+          values(b, k == 0, k + 1 == mine);
+          if (k + 1 < mine) scores(block(k + 1));
+        }
+        __syncwarp();
       }
 
       // ---- the piece's rows
@@ -823,25 +867,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
           if (live && a.lse) a.lse[orow] = none ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
         }
       }
-      umma::fence_before();
     }
-    blocks_done += nblk;
-    if (SPLIT) {
-      items_done[0] += both ? (nblk + 1) / 2 : nblk;
-      items_done[1] += both ? nblk / 2 : 0;
-    } else {
-      items_done[0] += nblk;
-      items_done[1] += both ? nblk : 0;
-    }
-    ++pieces_done[0];
-    pieces_done[1] += both;
-    at += nblk;
-    __syncthreads();
-    umma::fence_after();
   }
   if (tid == 0) p.desc[c] = desc;
   __syncthreads();
-  if (warp == 12) umma::dealloc(tmem, 512);
+  if (warp == 15) umma::dealloc(tmem, 512);
 }
 
 // Merges the pieces of the unit that starts last in CTA c's range and goes on
