@@ -22,24 +22,69 @@ __device__ __forceinline__ float log2_approx(float x) {
   return y;
 }
 
-// A factor s in [1, 2) whose products s c_k round to fp16 with the smallest
-// worst relative error over the 16 levels, out of 32 candidates (ties to the
-// smaller one).  The whole warp calls it; every lane gets s.  A single
-// rounding of the levels is a fixed error in every score and value, up to
-// 2^-11; the factor takes it to about a quarter of that.
-__device__ __forceinline__ float table_scale(const float *cent, int lane) {
-  const float s = 1.0f + (float)lane * (1.0f / 32.0f);
-  float worst = 0.f;
+// Scale of a table of fp16 levels.  The 16 levels c_k, rounded to fp16 once,
+// would be a fixed error of up to 2^-11 in every score and value; a factor s in
+// [1, 2) moves them to where fp16 holds them best.  What counts is the error
+// of a Gaussian coordinate's square, weighted by how often each level comes
+// up, apart from a gain common to all levels, which the kernels divide out:
+// over 192 candidates, one a thread, it falls from 2e-4 to 8e-5 of a
+// coordinate (d = 128; 4e-5 with 1024, for 5 us more a call).
+
+// P(|N(0,1)| in the level's cell) times the level squared, over their sum, for
+// the positive levels of the 16-level Lloyd-Max quantizer.
+__device__ constexpr float kLevelWeight[8] = {0.0033913f, 0.0296217f, 0.0772600f, 0.1365659f,
+                                               0.1927278f, 0.2258000f, 0.2113073f, 0.1233260f};
+
+// Gain sum w e and variance sum w e^2 - gain^2 of the relative errors e of the
+// levels c (rc = 1 / c); the difference of a value and its rounding is exact.
+__device__ __forceinline__ float level_error(const float (&c)[8], const float (&rc)[8], float s, float &gain) {
+  const float rs = __frcp_rn(s);
+  float m = 0.f, v = 0.f;
 #pragma unroll
-  for (int k = 8; k < 16; ++k) {
-    const float v = s * __ldg(cent + k);
-    worst = fmaxf(worst, fabsf(__half2float(__float2half_rn(v)) - v) / v);
+  for (int k = 0; k < 8; ++k) {
+    const float x = s * c[k], e = (__half2float(__float2half_rn(x)) - x) * (rc[k] * rs), we = kLevelWeight[k] * e;
+    m += we;
+    v = fmaf(we, e, v);
   }
-  // order by (error, lane)
-  unsigned key = (__float_as_uint(worst) & ~31u) | (unsigned)lane;
+  gain = m;
+  return fmaxf(v - m * m, 0.f);
+}
+
+__device__ __forceinline__ void load_levels(const float *cent, float (&c)[8], float (&rc)[8]) {
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) key = min(key, __shfl_xor_sync(dev::kFull, key, x));
-  return 1.0f + (float)(key & 31u) * (1.0f / 32.0f);
+  for (int k = 0; k < 8; ++k) {
+    c[k] = __ldg(cent + 8 + k);
+    rc[k] = __frcp_rn(c[k]);
+  }
+}
+
+// The best candidate into key[0] (the keys' table) and key[1] (the values'),
+// ties to the smaller; keys must be 0xffffffff before, with a barrier on both
+// sides.  All threads of the block call it, at most 512.
+__device__ __forceinline__ float candidate(int i, int n) { return 1.0f + (float)i / (float)n; }
+
+__device__ __forceinline__ void find_scales(const float *ck, const float *cv, int tid, int threads, unsigned *key) {
+  const int half = threads / 2, side = tid >= half;
+  const float *cent = side ? cv : ck;
+  float c[8], rc[8];
+  load_levels(cent, c, rc);
+  const int i = side ? tid - half : tid;
+  float gain;
+  const float v = level_error(c, rc, candidate(i, half), gain);
+  unsigned best = (__float_as_uint(v) & ~255u) | (unsigned)i;
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) best = min(best, __shfl_xor_sync(dev::kFull, best, x));
+  if ((tid & 31) == 0) atomicMin(key + side, best);
+}
+
+// The factor of a key, and in `unit` what table values are to be divided by.
+__device__ __forceinline__ float scale_of(unsigned key, int threads, const float *cent, float &unit) {
+  float c[8], rc[8], gain;
+  load_levels(cent, c, rc);
+  const float s = candidate((int)(key & 255u), threads / 2);
+  level_error(c, rc, s, gain);
+  unit = s * (1.0f + gain);
+  return s;
 }
 
 // D / 32 consecutive elements of a bf16 or fp16 row from element `at`.

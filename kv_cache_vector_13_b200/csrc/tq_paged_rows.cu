@@ -65,7 +65,8 @@ struct Low {
   __half q[2][8][D + 8];           // operand columns: hi of each row, lo of each row
   float f[kMaxRows];               // logit factor of each row
   float m[Cfg<D>::kWarps][kMaxRows], l[Cfg<D>::kWarps][kMaxRows];
-  float scale[2];                  // the tables' scales
+  float scale[2];                  // what the tables' values are to be divided by
+  unsigned key[2];
   float e[kMaxRows][Cfg<D>::kWarps], top[kMaxRows], sum[kMaxRows];  // merge of the warps
 };
 
@@ -79,6 +80,7 @@ struct RowsParams {
   PagedAttentionArgs a;
   float *slots;     // [2 * ctas][kMaxRows][D + 2]: sums, then M and L
   int4 *desc;       // [ctas]: {pieces, request, tile, head} of the unit that starts last in the CTA's range
+  float *v_unit;    // what the values' table is to be divided by
   unsigned *faults;
 };
 
@@ -213,16 +215,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
   }
   float *parts = reinterpret_cast<float *>(s_raw + (kPartAddr - dyn));  // [W][RT][PITCH]
 
-  // ---- the tables: entry e, lane l at 256 e + 4 l (keys) and + 128 (values)
-  if (warp < 2) {
-    const float *cent = warp == 0 ? a.kq.centroids : a.vq.centroids;
-    const float s = table_scale(cent, lane);
-    if (lane == 0) s_scale[warp] = s;
-    for (int e = lane; e < 256; e += 32) {
-      const __half2 h = __floats2half2_rn(s * __ldg(cent + (e & 15)), s * __ldg(cent + (e >> 4)));
-      reinterpret_cast<uint32_t *>(parts)[warp * 256 + e] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-  }
+  // ---- the tables' scales
+  if (tid < 2) sm.key[tid] = 0xffffffffu;
+  __syncthreads();
+  find_scales(a.kq.centroids, a.vq.centroids, tid, NT, sm.key);
   // ---- the line of steps: a run of requests a thread
   const int per = (a.R + NT - 1) / NT;
   int64_t mine = 0;
@@ -248,6 +244,21 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
     }
     s_base[tid] = base + x - mine;
   }
+  // ---- the tables: entry e, lane l at 256 e + 4 l (keys) and + 128 (values)
+  if (warp < 2) {
+    const float *cent = warp == 0 ? a.kq.centroids : a.vq.centroids;
+    float unit;
+    const float s = scale_of(sm.key[warp], NT, cent, unit);
+    if (lane == 0) {
+      s_scale[warp] = unit;
+      if (warp == 1 && c == 0) *p.v_unit = unit;  // for the merge
+    }
+    for (int e = lane; e < 256; e += 32) {
+      const __half2 h = __floats2half2_rn(s * __ldg(cent + (e & 15)), s * __ldg(cent + (e >> 4)));
+      reinterpret_cast<uint32_t *>(parts)[warp * 256 + e] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+  }
+  __syncthreads();
   {
     const uint32_t *pairs = reinterpret_cast<const uint32_t *>(parts);
     uint4 *tab = reinterpret_cast<uint4 *>(s_raw + (kTabAddr - dyn));
@@ -422,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
       for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 
     // The running softmax of the lane's rows over its tokens 8 i + g (value [i][o]: row o): scores in, weights
-    // times value norms out.  M is a reference that moves only when one of them would pass 2^8.
+    // times value norms out.  M is a reference that moves only when one of them would pass 2^14 (fp16 ends at 2^16).
     auto soft = [&](auto edge, int t0, uint32_t halves, float (&t)[4][2], const float (&kn)[4], const float (&vn)[4]) {
       constexpr bool EDGE = decltype(edge)::value;
       float lv[4], s[4][2], mx = -INFINITY;
@@ -440,7 +451,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
         }
         mx = fmaxf(mx, fmaxf(t[i][0], t[i][1]) + lv[i]);
       }
-      if (__any_sync(dev::kFull, mx > 8.f)) {
+      if (__any_sync(dev::kFull, mx > 14.f)) {
         float r2[2];
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
@@ -668,11 +679,11 @@ __global__ void __launch_bounds__(D * (P4 ? 4 : 8)) paged_merge_kernel(const __g
   __shared__ float s_e[RT][32], s_l[RT];
   const PagedAttentionArgs &a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
-  const float vs = table_scale(a.vq.centroids, lane);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int4 desc = __ldcg(p.desc + c);
   const int n = desc.x;
   if (n == 0) return;
+  const float vs = __ldcg(p.v_unit);
   const int G = a.Hq / a.Hkv;
   const Req req = load_req(a, desc.y, RT, p.faults);
   const int row0 = desc.z * RT, nrows = min(RT, req.n * G - row0);
@@ -759,15 +770,17 @@ cudaError_t run_d(const RowsParams &p, bool p4, cudaStream_t s) {
 
 size_t paged_rows_workspace(int d) {
   const size_t ctas = decode_ctas();
-  return ctas * sizeof(int4) + 2 * ctas * kMaxRows * (d + 2) * sizeof(float);
+  return ctas * sizeof(int4) + 16 + 2 * ctas * kMaxRows * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_rows(const PagedAttentionArgs &a, cudaStream_t s) {
-  RowsParams p{a, nullptr, nullptr, nullptr};
+  RowsParams p{};
+  p.a = a;
   const cudaError_t e = fault_word(&p.faults);
   if (e != cudaSuccess) return e;
   p.desc = static_cast<int4 *>(a.ws);
-  p.slots = reinterpret_cast<float *>(p.desc + decode_ctas());
+  p.v_unit = reinterpret_cast<float *>(p.desc + decode_ctas());
+  p.slots = p.v_unit + 4;
   const bool p4 = (int64_t)a.max_q * (a.Hq / a.Hkv) <= 4;
   return a.kq.d == 64 ? run_d<64>(p, p4, s) : run_d<128>(p, p4, s);
 }

@@ -55,12 +55,15 @@ struct Tile {
 struct TileParams {
   PagedAttentionArgs a;
   int rt;                  // rows per tile: 256 wide, 128 split
+  uint32_t page_mul;       // token / page_size = (token * page_mul) >> page_shift, below 2^31 tokens
+  int page_shift;
   const __half *qhi, *qlo; // [T * Hq][D] turned rows
   const float *qf;         // [T * Hq] the factor their scores still need (softmax scale, log2 e, row scale)
   int32_t *first;          // [R + 1] first tile of each request
   int64_t *line;           // [tiles + 1] blocks (of one KV head) before each tile
   float *slots;            // [2 * ctas][rt * (D + 2)]
   int4 *desc;              // [ctas]
+  float *v_unit;           // what the values' table is to be divided by
   unsigned *faults;
 };
 
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(256) paged_tile_prep_kernel(const __grid_const
   constexpr int E = 16, T = D / E, RPW = 32 / T;
   const int t = lane % T;
   const int64_t rows = a.T * a.Hq;
-  const float scale = a.scale * 1.4426950408889634f / (a.kq.sqrt_d * table_scale(a.kq.centroids, lane));
+  const float scale = a.scale * 1.4426950408889634f / a.kq.sqrt_d;
   uint32_t sg = 0;
 #pragma unroll
   for (int e = 0; e < E; ++e) sg |= (a.kq.signs[t * E + e] < 0 ? 1u : 0u) << e;
@@ -224,7 +227,7 @@ struct Piece {
   int starts, ends;  // whether they hold the unit's first and last block
 };
 
-constexpr int kNormBufs = 4;
+constexpr int kNormBufs = 8;
 
 struct Low {
   // A tile's blocks alternate between two barriers: with split blocks a set waits for every other one only.
@@ -236,7 +239,9 @@ struct Low {
   alignas(16) uint32_t valid[kNormBufs][kBlk / 32];
   float f[256];          // score factors of the rows
   float m[128], l[128];  // the odd set's references and sums (split)
-  float scale[2];
+  float scale[2];        // what the tables' values are to be divided by
+  unsigned key[2];
+  uint32_t sign[4];      // the value rotation's sign flips
 };
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
@@ -258,13 +263,18 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// D[tmem] (+)= A[tmem] B for one K = 16 step.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
-  const uint32_t z = 0u;
+// D[tmem] (+)= A B for one K = 16 step, A in shared memory, and in tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n}\n" ::"r"(d),
-      "r"(at), "l"(bdesc), "r"(idesc), "r"(accum), "r"(z), "r"(z), "r"(z), "r"(z));
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accum));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(at), "l"(bdesc), "r"(idesc), "r"(accum));
 }
 
 #define TQ_LIST16(v, b) "r"(v[b]), "r"(v[b + 1]), "r"(v[b + 2]), "r"(v[b + 3]), "r"(v[b + 4]), "r"(v[b + 5]), \
@@ -279,10 +289,19 @@ __device__ __forceinline__ void st32(uint32_t t, const uint32_t (&v)[32]) {
                "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::
                    TQ_LIST16(v, 0), TQ_LIST16(v, 16), "r"(t) : "memory");
 }
-__device__ __forceinline__ void ld8(uint32_t t, uint32_t (&v)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+// 16 columns on their way; their values are there behind wait16.
+__device__ __forceinline__ void ld16(uint32_t t, uint32_t (&v)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+               "%14, %15}, [%16];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                 "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
                : "r"(t));
+}
+__device__ __forceinline__ void wait16(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :: "memory");
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
@@ -314,13 +333,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
 
   // ---- the tables (see the rows kernel), barriers, tensor memory
   uint32_t *pairs = reinterpret_cast<uint32_t *>(s_raw + (kHighAddr - dyn));
+  if (tid < 2) sm.key[tid] = 0xffffffffu;
+  __syncthreads();
+  find_scales(a.kq.centroids, a.vq.centroids, tid, kThreads, sm.key);
+  __syncthreads();
   if (warp < 2) {
     const float *cent = warp == 0 ? a.kq.centroids : a.vq.centroids;
-    const float s = table_scale(cent, lane);
-    if (lane == 0) sm.scale[warp] = s;
+    float unit;
+    const float s = scale_of(sm.key[warp], kThreads, cent, unit);
+    if (lane == 0) {
+      sm.scale[warp] = unit;
+      if (warp == 1 && c == 0) *p.v_unit = unit;  // for the merge
+    }
     for (int e = lane; e < 256; e += 32) {
       const __half2 h = __floats2half2_rn(s * __ldg(cent + (e & 15)), s * __ldg(cent + (e >> 4)));
       pairs[warp * 256 + e] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+  }
+  if (warp == 2) {
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      const unsigned m = __ballot_sync(dev::kFull, a.vq.signs[32 * w + lane] < 0);
+      if (lane == 0) sm.sign[w] = m;
     }
   }
   if (warp == 15) umma::alloc(&sm.tmem, 512);
@@ -449,21 +483,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
     nblk = q.b1 - q.b0;
     both = SPLIT ? nblk > 1 : q.nrows > 128;
     // ---- query rows into the operand tiles: 16-byte words of 8 coordinates
-    for (int i = tid; i < RT * (D / 8); i += kThreads) {
-      const int row = i / D * 8 + (i & 7), w = (i >> 3) % (D / 8);
-      uint4 x = make_uint4(0, 0, 0, 0), y = x;
+    constexpr int QB = RT * (D / 8) / kThreads;  // a thread's words, their loads in flight together
+    uint4 qx[QB], qy[HL ? QB : 1];
+#pragma unroll
+    for (int n = 0; n < QB; ++n) {
+      const int i = n * kThreads + tid, row = i / D * 8 + (i & 7), w = (i >> 3) % (D / 8);
+      qx[n] = make_uint4(0, 0, 0, 0);
+      if (HL) qy[HL ? n : 0] = qx[n];
       if (row < q.nrows) {
         const int qi = (q.row0 + row) / G;
         const int64_t src = (int64_t)(q.q0 + qi) * a.Hq + q.h * G + (q.row0 + row - qi * G);
-        x = __ldcg(reinterpret_cast<const uint4 *>(p.qhi + src * D) + w);
-        if (HL) y = __ldcg(reinterpret_cast<const uint4 *>(p.qlo + src * D) + w);
-        if (w == 0) sm.f[row] = __ldcg(p.qf + src);
-      } else if (w == 0) {
-        sm.f[row] = 0.f;
+        qx[n] = __ldcg(reinterpret_cast<const uint4 *>(p.qhi + src * D) + w);
+        if (HL) qy[HL ? n : 0] = __ldcg(reinterpret_cast<const uint4 *>(p.qlo + src * D) + w);
       }
+    }
+    if (tid < RT) {
+      float f = 0.f;
+      if (tid < q.nrows) {
+        const int qi = (q.row0 + tid) / G;
+        f = __ldcg(p.qf + (int64_t)(q.q0 + qi) * a.Hq + q.h * G + (q.row0 + tid - qi * G));
+      }
+        sm.f[tid] = f / sm.scale[0];
+    }
+#pragma unroll
+    for (int n = 0; n < QB; ++n) {
+      const int i = n * kThreads + tid, row = i / D * 8 + (i & 7), w = (i >> 3) % (D / 8);
       const uint32_t o = ((row & 127) >> 3) * GB + w * 128 + (row & 7) * 16;
-      sts128((row < 128 ? kQ0 : kQ1) + o, x.x, x.y, x.z, x.w);
-      if (HL) sts128(kQ1 + o, y.x, y.y, y.z, y.w);
+      sts128((row < 128 ? kQ0 : kQ1) + o, qx[n].x, qx[n].y, qx[n].z, qx[n].w);
+      if (HL) sts128(kQ1 + o, qy[HL ? n : 0].x, qy[HL ? n : 0].y, qy[HL ? n : 0].z, qy[HL ? n : 0].w);
     }
     umma::fence_async_smem();
     __syncthreads();
@@ -486,42 +533,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
     while (next_piece()) {
       const int32_t *row = a.table + (int64_t)q.r * a.table_stride;
       // page of token 32 wq + lane of block b (none is needed: -1), and its record
-      auto page_id = [&](int b) {
-        const int j = b * kBlk + 32 * wq + lane;
-        return b < q.b1 && j >= q.first && j < q.kv ? __ldg(row + j / a.page_size) : -1;
-      };
+      auto token = [&](int b) { return b * kBlk + 32 * wq + lane; };
+      auto page = [&](int j) { return (int)(((uint64_t)(uint32_t)j * p.page_mul) >> p.page_shift); };
+      auto wanted = [&](int b) { return b < q.b1 && token(b) >= q.first && token(b) < q.kv; };
+      auto page_id = [&](int b) { return wanted(b) ? __ldg(row + page(token(b))) : -1; };
       auto record = [&](int b, int id) -> int64_t {
-        const int j = b * kBlk + 32 * wq + lane, off = j % a.page_size;
-        if (b >= q.b1 || j < q.first || j >= q.kv) return -1;
+        if (!wanted(b)) return -1;
         if ((unsigned)id >= (unsigned)a.n_pages) {
           atomicOr(p.faults, kFaultIndex);
           return -1;
         }
+        const int j = token(b), off = j - page(j) * a.page_size;
         return id * cv.sb + q.h * cv.sh + off * cv.sn;
       };
       uint4 x[IT];
-      float norm;
-      // 16 code bytes of the lane's token of each pass (the record comes from the lane that has it), and the norm
-      // of token 32 wq + lane
+      // 16 code bytes of the lane's token of each pass; the record comes from the lane that has it
       auto load = [&](int64_t rec) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           const int64_t r1 = __shfl_sync(dev::kFull, rec, TPI * i + tk);
           x[i] = r1 >= 0 ? __ldg(reinterpret_cast<const uint4 *>(cv.codes + r1 * (D / 2)) + ch) : make_uint4(0, 0, 0, 0);
         }
-        norm = rec >= 0 ? __ldg(cv.norms + rec) : 0.f;
       };
-      // a block's page numbers are read two blocks ahead, its codes and norms one block ahead
-      int64_t rec = record(q.b0, page_id(q.b0));
-      load(rec);
-      bool have = rec >= 0;
-      rec = record(q.b0 + 1, page_id(q.b0 + 1));
-      for (int b = 0; b < nblk; ++b) {
-        const uint32_t u = blocks_done + b;
+      auto load_norm = [&](int64_t rec) { return rec >= 0 ? __ldg(cv.norms + rec) : 0.f; };
+      // Block u's norms of token 32 wq + lane.  They go out a block ahead of the codes; the buffer was block
+      // u - 8's, whose weights are long in a product that this thread has seen done.
+      auto publish = [&](uint32_t u, float norm, bool have) {
         const int nb = u % kNormBufs;
-        const int id2 = page_id(q.b0 + b + 2);
-        // Free: the buffer was block u - 4's.  This thread has seen the scores of block u - 2 done (or its
-        // values), which were issued behind the products with the weights of block u - 4 (or u - 3 and u - 4).
         if (is_k) {
           sm.kn[nb][32 * wq + lane] = norm;
           const unsigned ok = __ballot_sync(dev::kFull, have);
@@ -531,6 +569,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
           sm.lv[nb][32 * wq + lane] = fmaxf(log2_approx(norm), -64.f);
         }
         arrive(bar(sm.n_full[nb]));
+      };
+      // Page numbers are read three blocks ahead, norms two, codes one.  A block's loads leave together at its end and
+      // are used from the next one's start on: a load in between would be waited for with them.
+      int id1 = page_id(q.b0 + 1), id2 = page_id(q.b0 + 2);
+      const int64_t rec0 = record(q.b0, page_id(q.b0));
+      load(rec0);
+      publish(blocks_done, load_norm(rec0), rec0 >= 0);
+      int64_t rec = record(q.b0 + 1, id1);
+      float norm = load_norm(rec);
+      for (int b = 0; b < nblk; ++b) {
+        const uint32_t u = blocks_done + b;
+        if (b + 1 < nblk) publish(u + 1, norm, rec >= 0);
+        const int64_t rec2 = record(q.b0 + b + 2, id2);
         if (u > 0) wait(is_k ? sm.k_free : sm.v_free, u - 1);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
@@ -551,8 +602,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         umma::fence_async_smem();
         arrive(bar(is_k ? sm.k_full[u & 1] : sm.v_full[u & 1]));
         load(rec);
-        have = rec >= 0;
-        rec = record(q.b0 + b + 2, id2);
+        norm = load_norm(rec2);
+        id2 = page_id(q.b0 + b + 3);
+        rec = rec2;
       }
     }
   } else {
@@ -563,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const int i = SPLIT ? row : 128 * x + row;  // row of the tile
       const bool live = i < q.nrows;
-      int see_lo = 0, see_hi = INT_MAX;  // rows that are not there see everything (and go nowhere)
+      int see_lo = 0, see_hi = INT_MAX;  // a lane without a row sees everything (and goes nowhere)
       if (live) {
         const int pos = q.kv - q.n + (q.row0 + i) / G;
         see_hi = a.causal ? max(pos + 1, 0) : q.kv;
@@ -587,10 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         for (int s = 0; s < D / 16; ++s) {
           const uint64_t kd = umma::desc(kK + s * 256, 128, GB);
           if (HL) {
-            umma::mma_f16(s_col(x), umma::desc(kQ0 + s * 256, 128, GB), kd, kIdS, s > 0);
-            umma::mma_f16(s_col(x), umma::desc(kQ1 + s * 256, 128, GB), kd, kIdS, 1);
+            mma_ss(s_col(x), umma::desc(kQ0 + s * 256, 128, GB), kd, kIdS, s > 0);
+            mma_ss(s_col(x), umma::desc(kQ1 + s * 256, 128, GB), kd, kIdS, 1);
           } else {
-            umma::mma_f16(s_col(x), umma::desc((SPLIT || x == 0 ? kQ0 : kQ1) + s * 256, 128, GB), kd, kIdS, s > 0);
+            mma_ss(s_col(x), umma::desc((SPLIT || x == 0 ? kQ0 : kQ1) + s * 256, 128, GB), kd, kIdS, s > 0);
           }
         }
         umma::commit(bar(sm.s_full[x]));
@@ -611,6 +663,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         if (last) umma::commit(bar(sm.o_fin[x]));
       };
       const int mine = x < (both ? 2 : 1) ? (SPLIT ? (both ? (nblk + 1 - x) / 2 : nblk) : nblk) : 0;
+      // The sets take turns at the softmax, one's products meanwhile: left alone they fall into step, and the
+      // tensor cores and the other pipes idle in turn.  Barrier 4 lets the even set go on, 5 the odd one.
+      const int turns[2] = {mine, both ? (SPLIT ? (x == 0 ? nblk / 2 : (nblk + 1) / 2) : nblk) : 0};  // mine, the other's
+      if (both && x == 1) asm volatile("bar.arrive 4, 256;" ::: "memory");
       if (mine > 0 && issuer) scores(block(0));
       __syncwarp();
       for (int k = 0; k < mine; ++k) {
@@ -620,6 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         wait(sm.n_full[nb], u / kNormBufs);
         wait(sm.s_full[x], items_done[x] + k);
         umma::fence_after();
+        if (both) {
+          if (x == 0) asm volatile("bar.sync 4, 256;" ::: "memory");
+          else asm volatile("bar.sync 5, 256;" ::: "memory");
+        }
         const uint4 vm = *reinterpret_cast<const uint4 *>(sm.valid[nb]);
         const uint32_t valid[4] = {vm.x, vm.y, vm.z, vm.w};
         const bool whole = see_lo <= j0 && see_hi >= j0 + kBlk && (vm.x & vm.y & vm.z & vm.w) == ~0u;
@@ -629,20 +689,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
           const uint32_t m = hi <= 0 || lo >= 32 ? 0u : (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
           return m & valid[r];
         };
+        // fn(c, columns 16 c .. 16 c + 15) over the row's scores, the next 16 on their way meanwhile
+        auto runs = [&](auto &&fn) {
+          uint32_t s[2][16];
+          ld16(s_col(x) + lanes, s[0]);
+#pragma unroll
+          for (int c8 = 0; c8 < 8; ++c8) {
+            wait16(s[c8 & 1]);
+            if (c8 < 7) ld16(s_col(x) + lanes + 16 * (c8 + 1), s[(c8 + 1) & 1]);
+            fn(c8, s[c8 & 1]);
+          }
+        };
         // the largest logit + log2 ||v|| of the row
         auto top = [&](auto edge) {
           constexpr bool EDGE = decltype(edge)::value;
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          runs([&](int c8, const uint32_t (&s)[16]) {
+            const uint32_t m = EDGE ? mask(c8 >> 1) >> (16 * (c8 & 1)) : ~0u;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            uint32_t s[32];
-            umma::ld32(s_col(x) + lanes + 32 * r, s);
-            umma::wait_ld();
-            const uint32_t m = EDGE ? mask(r) : ~0u;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 kn = *reinterpret_cast<const float4 *>(kns + 32 * r + e);
-              const float4 lv = *reinterpret_cast<const float4 *>(lvs + 32 * r + e);
+            for (int e = 0; e < 16; e += 4) {
+              const float4 kn = *reinterpret_cast<const float4 *>(kns + 16 * c8 + e);
+              const float4 lv = *reinterpret_cast<const float4 *>(lvs + 16 * c8 + e);
               float k0, k1, k2, k3, t[4];
               dev::mul_x2(k0, k1, kn.x, kn.y, f, f);
               dev::mul_x2(k2, k3, kn.z, kn.w, f, f);
@@ -652,21 +719,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
               for (int o = 0; o < 4; ++o)
                 if (!EDGE || (m >> (e + o) & 1)) mx[o] = fmaxf(mx[o], t[o]);
             }
-          }
+          });
           return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         };
-        // Weights relative to M, of run r: their sum, and times ||v|| as operand words (hi, and with HL lo).
-        auto weights = [&](auto edge, int r, float &sum, uint32_t *w, uint32_t *wl) {
+        // Weights relative to M of 16 columns: their sums, and times ||v|| as operand words (hi, and with HL lo).
+        auto weights = [&](auto edge, int c8, const uint32_t (&s)[16], float (&sum)[2], uint32_t *w, uint32_t *wl) {
           constexpr bool EDGE = decltype(edge)::value;
-          uint32_t s[32];
-          umma::ld32(s_col(x) + lanes + 32 * r, s);
-          umma::wait_ld();
-          const uint32_t m = EDGE ? mask(r) : ~0u;
-          float l0 = 0.f, l1 = 0.f;
+          const uint32_t m = EDGE ? mask(c8 >> 1) >> (16 * (c8 & 1)) : ~0u;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 kn = *reinterpret_cast<const float4 *>(kns + 32 * r + e);
-            const float4 vn = *reinterpret_cast<const float4 *>(vns + 32 * r + e);
+          for (int e = 0; e < 16; e += 4) {
+            const float4 kn = *reinterpret_cast<const float4 *>(kns + 16 * c8 + e);
+            const float4 vn = *reinterpret_cast<const float4 *>(vns + 16 * c8 + e);
             float k0, k1, k2, k3, t[4];
             dev::mul_x2(k0, k1, kn.x, kn.y, f, f);
             dev::mul_x2(k2, k3, kn.z, kn.w, f, f);
@@ -677,8 +740,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
               t[o] = exp2_approx(t[o]);
               if (EDGE) t[o] = m >> (e + o) & 1 ? t[o] : 0.f;
             }
-            dev::add_x2(l0, l1, l0, l1, t[0], t[1]);
-            dev::add_x2(l0, l1, l0, l1, t[2], t[3]);
+            dev::add_x2(sum[0], sum[1], sum[0], sum[1], t[0], t[1]);
+            dev::add_x2(sum[0], sum[1], sum[0], sum[1], t[2], t[3]);
             dev::mul_x2(t[0], t[1], t[0], t[1], vn.x, vn.y);
             dev::mul_x2(t[2], t[3], t[2], t[3], vn.z, vn.w);
 #pragma unroll
@@ -696,7 +759,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
               }
             }
           }
-          sum += l0 + l1;
         };
         // moves the reference M to the block's largest value if that is above it
         auto move = [&](float mx) {
@@ -715,45 +777,54 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
             }
           }
         };
-        // M moves only when a weight times its norm would pass 2^8: with HL that is looked for before the
+        // M moves only when a weight times its norm would pass 2^14 (fp16 ends at 2^16): with HL that is looked for before the
         // weights, which take the scores' place at once; else the weights are kept in registers, and where one
         // is too large they are made again
         auto item = [&](auto edge) {
-          float sum = 0.f;
+          float sum[2] = {0.f, 0.f};
           if constexpr (HL) {
             const float mx = top(edge);
-            if (__any_sync(dev::kFull, mx > M + 8.f)) move(mx);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              uint32_t w[16], wl[16];
-              weights(edge, r, sum, w, wl);
-              st16(s_col(x) + lanes + 32 * r, w);
-              st16(s_col(x) + lanes + 32 * r + 16, wl);
-            }
+            if (__any_sync(dev::kFull, mx > M + 14.f)) move(mx);
+            uint32_t w[16], wl[16];
+            runs([&](int c8, const uint32_t (&s)[16]) {
+              weights(edge, c8, s, sum, w + 8 * (c8 & 1), wl + 8 * (c8 & 1));
+              if (c8 & 1) {
+                st16(s_col(x) + lanes + 16 * (c8 - 1), w);
+                st16(s_col(x) + lanes + 16 * c8, wl);
+              }
+            });
           } else {
             uint32_t w[4][16];
             bool again = k == 0;
             for (;;) {
               if (again) move(top(edge));
-              sum = 0.f;
+              sum[0] = sum[1] = 0.f;
               __half2 most = __float2half2_rn(0.f);
+              runs([&](int c8, const uint32_t (&s)[16]) {
+                uint32_t *to = w[c8 >> 1] + 8 * (c8 & 1);
+                weights(edge, c8, s, sum, to, nullptr);
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                weights(edge, r, sum, w[r], nullptr);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) most = __hmax2(most, *reinterpret_cast<const __half2 *>(&w[r][e]));
-              }
+                for (int e = 0; e < 8; ++e) most = __hmax2(most, *reinterpret_cast<const __half2 *>(to + e));
+              });
               // a reference that has just moved bounds the weights by 1 (and rounding)
-              if (again || !__any_sync(dev::kFull, __hgt(__hmax(__low2half(most), __high2half(most)), __float2half(256.f)))) break;
+              const __half2 wide = __half2half2(__float2half(16384.f));
+              if (again || !__any_sync(dev::kFull, !__hbgt2(wide, most))) break;
               again = true;
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) st16(s_col(x) + lanes + 32 * r, w[r]);
           }
-          l += sum;
+          l += sum[0] + sum[1];
         };
-        if (__all_sync(dev::kFull, whole)) item(std::false_type{});
-        else item(std::true_type{});
+        // a warp without a row leaves its weights as they are: nothing reads what comes of them
+        if (__any_sync(dev::kFull, live)) {
+          if (__all_sync(dev::kFull, whole || !live)) item(std::false_type{});
+          else item(std::true_type{});
+        }
+        if (both) {  // the other set's turn, if it has another
+          if (x == 0 && k < turns[1]) asm volatile("bar.arrive 5, 256;" ::: "memory");
+          if (x == 1 && k + 1 < turns[1]) asm volatile("bar.arrive 4, 256;" ::: "memory");
+        }
         wait_st();
         umma::fence_before();
         // every row's weights are in place: the products with them, and the set's next scores behind those
@@ -791,80 +862,55 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         const bool done = q.starts && q.ends;
         float *slot = p.slots + (size_t)(2 * c + (q.starts ? 1 : 0)) * RT * (D + 2);
         const float inv = 1.0f / (l * a.vq.sqrt_d * sm.scale[1]);
+        float y[D];
 #pragma unroll
         for (int r = 0; r < NC; ++r) {
           uint32_t o[32];
-          float y[32];
           umma::ld32(o_col(x) + lanes + 32 * r, o);
           umma::wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]);
+          for (int e = 0; e < 32; ++e) y[32 * r + e] = __uint_as_float(o[e]);
           if (SPLIT && both) {
             umma::ld32(o_col(1) + lanes + 32 * r, o);
             umma::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = y[e] * f0 + __uint_as_float(o[e]) * f1;
-          }
-          if (done) {  // inverse rotation: within the run here, over the runs below
-            dev::fwht_local<32>(y);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(y[e]);
-            st32(o_col(x) + lanes + 32 * r, o);
-          } else if (live) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4 *>(slot + ((size_t)(8 * r + e / 4) * RT + i) * 4) =
-                  make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+            for (int e = 0; e < 32; ++e) y[32 * r + e] = y[32 * r + e] * f0 + __uint_as_float(o[e]) * f1;
           }
         }
         if (!done && live) {
+#pragma unroll
+          for (int e = 0; e < D; e += 4)
+            *reinterpret_cast<float4 *>(slot + ((size_t)(e / 4) * RT + i) * 4) =
+                make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
           slot[(size_t)D * RT + i] = M;
           slot[(size_t)(D + 1) * RT + i] = l;
         }
-        if (done) {
-          wait_st();
+        if (done && live) {  // inverse rotation of the thread's row
+          dev::fwht_local<D>(y);
           const bool none = l == 0.f;  // no token seen
           const int qi = (q.row0 + i) / G;
           const int64_t orow = (int64_t)(q.q0 + qi) * a.Hq + q.h * G + (q.row0 + i - qi * G);
           uint16_t *out = static_cast<uint16_t *>(a.out) + orow * D;
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            uint32_t v[NC][8];
+          for (int j = 0; j < D; j += 8) {
+            uint32_t w[4];
 #pragma unroll
-            for (int r = 0; r < NC; ++r) ld8(o_col(x) + lanes + 32 * r + j, v[r]);
-            umma::wait_ld();
-            float y[NC][8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float z[NC];
-#pragma unroll
-              for (int r = 0; r < NC; ++r) z[r] = __uint_as_float(v[r][e]);
-              dev::fwht_local<NC>(z);
-#pragma unroll
-              for (int r = 0; r < NC; ++r) y[r][e] = z[r];
-            }
-            if (live) {
-#pragma unroll
-              for (int r = 0; r < NC; ++r) {
-                const int8_t *sg = a.vq.signs + 32 * r + j;
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float u = none ? 0.f : y[r][2 * e] * inv * (float)__ldg(sg + 2 * e);
-                  const float t = none ? 0.f : y[r][2 * e + 1] * inv * (float)__ldg(sg + 2 * e + 1);
-                  if (a.dtype == TQ_BF16) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(u, t);
-                    w[e] = *reinterpret_cast<const uint32_t *>(&h);
-                  } else {
-                    const __half2 h = __floats2half2_rn(u, t);
-                    w[e] = *reinterpret_cast<const uint32_t *>(&h);
-                  }
-                }
-                *reinterpret_cast<uint4 *>(out + 32 * r + j) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 4; ++e) {
+              // bit j + 2 e of the sign masks: -1
+              const uint32_t sg = sm.sign[j / 32] >> (j % 32 + 2 * e);
+              const float u = none ? 0.f : __uint_as_float(__float_as_uint(y[j + 2 * e] * inv) ^ (sg << 31));
+              const float t = none ? 0.f : __uint_as_float(__float_as_uint(y[j + 2 * e + 1] * inv) ^ ((sg >> 1) << 31));
+              if (a.dtype == TQ_BF16) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(u, t);
+                w[e] = *reinterpret_cast<const uint32_t *>(&h);
+              } else {
+                const __half2 h = __floats2half2_rn(u, t);
+                w[e] = *reinterpret_cast<const uint32_t *>(&h);
               }
             }
+            *reinterpret_cast<uint4 *>(out + j) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          if (live && a.lse) a.lse[orow] = none ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
+          if (a.lse) a.lse[orow] = none ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
         }
       }
     }
@@ -880,10 +926,10 @@ template <int D>
 __global__ void __launch_bounds__(256) paged_tile_merge_kernel(const __grid_constant__ TileParams p) {
   const PagedAttentionArgs &a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x, RT = p.rt;
-  const float vs = table_scale(a.vq.centroids, lane);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int4 desc = __ldcg(p.desc + c);
   if (desc.x == 0) return;
+  const float vs = __ldcg(p.v_unit);
   const int G = a.Hq / a.Hkv;
   const Req req = load_req(a, desc.y, p.faults);
   const int row0 = desc.z * RT, nrows = min(RT, req.n * G - row0);
@@ -921,7 +967,7 @@ Layout layout(int R, int64_t T, int Hq, int Hkv, int d) {
   const size_t ctas = decode_ctas();
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   Layout l;
-  l.slots = up(ctas * sizeof(int4));
+  l.slots = up(ctas * sizeof(int4) + sizeof(float));
   l.first = up(l.slots + 2 * ctas * 256 * (d + 2) * sizeof(float));
   l.line = up(l.first + ((size_t)R + 1) * 4);
   const size_t tiles = (size_t)T * (Hq / Hkv) / 128 + R + 1;  // at most, in tiles of 128 rows
@@ -977,10 +1023,12 @@ cudaError_t launch_paged_tile(const PagedAttentionArgs &a, cudaStream_t s) {
   const cudaError_t e = fault_word(&p.faults);
   if (e != cudaSuccess) return e;
   // few rows a unit, or fp16 outputs: the blocks are split over the two sets instead of the rows
+  dev::magic31_div(a.page_size, p.page_mul, p.page_shift);
   p.rt = a.dtype == TQ_F16 || (int64_t)a.max_q * (a.Hq / a.Hkv) <= 128 ? 128 : 256;
   const Layout l = layout(a.R, a.T, a.Hq, a.Hkv, a.kq.d);
   char *w = static_cast<char *>(a.ws);
   p.desc = reinterpret_cast<int4 *>(w);
+  p.v_unit = reinterpret_cast<float *>(p.desc + decode_ctas());
   p.slots = reinterpret_cast<float *>(w + l.slots);
   p.first = reinterpret_cast<int32_t *>(w + l.first);
   p.line = reinterpret_cast<int64_t *>(w + l.line);
