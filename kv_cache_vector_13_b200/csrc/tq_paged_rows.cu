@@ -40,6 +40,7 @@ constexpr int kStep = 32;                // tokens per step, in two halves of 16
 constexpr uint32_t kTabAddr = 0x10000u;  // the pair tables: 64 KiB at this shared address
 constexpr uint32_t kPartAddr = 0x20000u; // the warps' partial sums
 constexpr int kMaxRows = 8;
+constexpr int64_t kSteps = ((int64_t)1 << 42) - 1;
 constexpr int kStages = 2;               // a warp's steps in shared memory: one worked on, one on its way
 
 template <int D>
@@ -67,6 +68,7 @@ struct Low {
   float m[Cfg<D>::kWarps][kMaxRows], l[Cfg<D>::kWarps][kMaxRows];
   float scale[2];                  // what the tables' values are to be divided by
   unsigned key[2];
+  __half level[2][16];             // the scaled levels
   float e[kMaxRows][Cfg<D>::kWarps], top[kMaxRows], sum[kMaxRows];  // merge of the warps
 };
 
@@ -79,7 +81,7 @@ __host__ __device__ constexpr uint32_t smem_end() {
 struct RowsParams {
   PagedAttentionArgs a;
   float *slots;     // [2 * ctas][kMaxRows][D + 2]: sums, then M and L
-  int4 *desc;       // [ctas]: {pieces, request, tile, head} of the unit that starts last in the CTA's range
+  int4 *desc;       // [2 * ctas]: {pieces, rows, first row, head}, {first query row} of the unit that starts last in a range
   float *v_unit;    // what the values' table is to be divided by
   unsigned *faults;
 };
@@ -209,22 +211,24 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
   if (dyn + sizeof(Low<D>) + (W - Cfg<D>::kHigh) * Cfg<D>::kRing > kTabAddr || dyn + dyn_bytes < smem_end<D>()) {
     if (tid == 0) {
       atomicOr(p.faults, kFaultSmemLayout);
-      p.desc[c] = make_int4(0, 0, 0, 0);
+      p.desc[2 * c] = make_int4(0, 0, 0, 0);
     }
     return;
   }
   float *parts = reinterpret_cast<float *>(s_raw + (kPartAddr - dyn));  // [W][RT][PITCH]
 
-  // ---- the tables' scales
+  // ---- the tables' scales, and the line of steps: a run of requests a thread
   if (tid < 2) sm.key[tid] = 0xffffffffu;
+  const int per = (a.R + NT - 1) / NT;
+  int64_t mine = 0;  // steps, and units from bit 42 on
+  for (int r = tid * per; r < min((tid + 1) * per, a.R); ++r) {
+    const Req q = load_req(a, r, RT, p.faults);
+    mine += weight(q, a.Hkv) + (int64_t)((uint64_t)q.tiles * (uint64_t)a.Hkv << 42);
+  }
   __syncthreads();
   find_scales(a.kq.centroids, a.vq.centroids, tid, NT, sm.key);
-  // ---- the line of steps: a run of requests a thread
-  const int per = (a.R + NT - 1) / NT;
-  int64_t mine = 0;
-  for (int r = tid * per; r < min((tid + 1) * per, a.R); ++r)
-    mine += weight(load_req(a, r, RT, p.faults), a.Hkv);
   int64_t total;
+  int units;
   {
     int64_t x = mine;
 #pragma unroll
@@ -242,38 +246,24 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
       if (i < warp) base += y;
       total += y;
     }
-    s_base[tid] = base + x - mine;
-  }
-  // ---- the tables: entry e, lane l at 256 e + 4 l (keys) and + 128 (values)
-  if (warp < 2) {
-    const float *cent = warp == 0 ? a.kq.centroids : a.vq.centroids;
-    float unit;
-    const float s = scale_of(sm.key[warp], NT, cent, unit);
-    if (lane == 0) {
-      s_scale[warp] = unit;
-      if (warp == 1 && c == 0) *p.v_unit = unit;  // for the merge
-    }
-    for (int e = lane; e < 256; e += 32) {
-      const __half2 h = __floats2half2_rn(s * __ldg(cent + (e & 15)), s * __ldg(cent + (e >> 4)));
-      reinterpret_cast<uint32_t *>(parts)[warp * 256 + e] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-  }
-  __syncthreads();
-  {
-    const uint32_t *pairs = reinterpret_cast<const uint32_t *>(parts);
-    uint4 *tab = reinterpret_cast<uint4 *>(s_raw + (kTabAddr - dyn));
-    for (int i = tid; i < 256 * 16; i += NT) {
-      const uint32_t w = pairs[((i >> 3) & 1) * 256 + (i >> 4)];
-      tab[i] = make_uint4(w, w, w, w);
-    }
+    units = (int)(total >> 42);
+    total &= kSteps;
+    s_base[tid] = (base + x - mine) & kSteps;
   }
   __syncthreads();
 
-  // every range has a step at least, so no piece of a unit is missing
-  const int ctas = (int)min((int64_t)gridDim.x, total);
-  int64_t at = c < ctas ? total * c / ctas : 0;
-  const int64_t end = c < ctas ? total * (c + 1) / ctas : 0;
-  int4 desc = make_int4(0, 0, 0, 0);
+  // Ranges.  Where the units are fewer than the CTAs, a multiple of them that idles at most a twentieth of the SMs:
+  // equally long units are then cut evenly and no CTA has parts of two (1 x 32768 tokens, 8 KV heads: 144 CTAs).
+  // Every range has a step at least, so no piece of a unit is missing.
+  int ctas = (int)gridDim.x;
+  if (units > 0 && units <= ctas && 20 * (ctas % units) <= ctas) ctas -= ctas % units;
+  ctas = (int)min((int64_t)ctas, total);
+  auto cut = [&](int i) {
+    return total < (1 << 21) ? (int64_t)((uint32_t)total * (uint32_t)i / (uint32_t)ctas) : total * i / ctas;
+  };
+  int64_t at = c < ctas ? cut(c) : 0;
+  const int64_t end = c < ctas ? cut(c + 1) : 0;
+  int4 desc = make_int4(0, 0, 0, 0), where = desc;
   // the request of the range's start
   int r = 0;
   int64_t r_base = 0;
@@ -296,8 +286,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
   uint32_t ktab, vtab;  // opaque, so that a table address stays one byte permute
   asm("mov.b32 %0, %1;" : "=r"(ktab) : "r"(kTabAddr + 4 * lane));
   asm("mov.b32 %0, %1;" : "=r"(vtab) : "r"(kTabAddr + 4 * lane + 128));
-  const float kscale = a.scale * 1.4426950408889634f / (a.kq.sqrt_d * s_scale[0]);
-  const float vscale = 1.0f / (a.vq.sqrt_d * s_scale[1]);
 
   // the lane's 16 bytes of a half's records (of its first 8 tokens for d = 128) and its norm, and where they go
   const int64_t k_tok = a.k.sn * (D / 2), v_tok = a.v.sn * (D / 2);
@@ -311,11 +299,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
   const uint32_t ring = warp < Cfg<D>::kHigh ? kPartAddr + warp * Cfg<D>::kRing
                                              : kTabAddr - (warp - Cfg<D>::kHigh + 1) * Cfg<D>::kRing;
 
-  while (at < end && r < a.R) {
+  for (bool tables = false; at < end && r < a.R; tables = true) {
     // ---- the piece: steps [s0, s1) of unit (r, h, tile)
     const int len = req.hi - req.lo;
     const int64_t x = at - r_base;
-    const int unit = (int)(x / len);
+    const int unit = x < INT_MAX ? (int)((uint32_t)x / (uint32_t)len) : (int)(x / len);
     const int s0 = req.lo + (int)(x - (int64_t)unit * len);
     const int s1 = (int)min((int64_t)req.hi, s0 + (end - at));
     const int h = unit / req.tiles, tile = unit - h * req.tiles;
@@ -371,6 +359,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
       find(4, krec2, vrec2);
       issue(0);
     }
+
+    if (!tables) {
+      // ---- the tables, while the first records are on their way: entry e, lane l at 256 e + 4 l (keys) and + 128
+      if (warp < 2) {
+        const float *cent = warp == 0 ? a.kq.centroids : a.vq.centroids;
+        float unit;
+        const float s = scale_of(sm.key[warp], NT, cent, unit);
+        if (lane < 16) sm.level[warp][lane] = __float2half_rn(s * __ldg(cent + lane));
+        if (lane == 0) {
+          s_scale[warp] = unit;
+          if (warp == 1 && c == 0) *p.v_unit = unit;  // for the merge
+        }
+      }
+      __syncthreads();
+      uint4 *tab = reinterpret_cast<uint4 *>(s_raw + (kTabAddr - dyn));
+      for (int i = tid; i < 256 * 16; i += NT) {
+        const __half *lv = sm.level[(i >> 3) & 1];
+        const __half2 h = __halves2half2(lv[(i >> 4) & 15], lv[i >> 8]);
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(&h);
+        tab[i] = make_uint4(w, w, w, w);
+      }
+    }
+    const float kscale = a.scale * 1.4426950408889634f / (a.kq.sqrt_d * s_scale[0]);
+    const float vscale = 1.0f / (a.vq.sqrt_d * s_scale[1]);
 
     // ---- query rows: sign flips, FWHT, a power of two that brings the largest into [1, 2)
     for (int i = warp; i < RT; i += W) {
@@ -651,10 +663,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
     if (starts && !ends) {
       // CTAs whose ranges the unit reaches: the last holds its last step
       const int64_t last = at + len - 1;
-      int64_t e = last * ctas / total;  // a first guess, put right below
-      while (e < ctas - 1 && total * (e + 1) / ctas <= last) ++e;
-      while (e > c && total * e / ctas > last) --e;
-      desc = make_int4((int)e - c + 1, r, tile, h);
+      int e = c;
+      if (last >= end) {
+        e = (int)(last * ctas / total);  // a first guess
+        while (e < ctas - 1 && cut(e + 1) <= last) ++e;
+        while (e > c && cut(e) > last) --e;
+      }
+      desc = make_int4(e - c + 1, nrows, row0, h);
+      where = make_int4(req.q0, 0, 0, 0);
     }
     __syncthreads();
     at += s1 - s0;
@@ -666,7 +682,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
       }
     }
   }
-  if (tid == 0) p.desc[c] = desc;
+  if (tid == 0) {
+    p.desc[2 * c] = desc;
+    p.desc[2 * c + 1] = where;
+  }
 }
 
 // Merges the pieces of the unit that starts last in CTA c's range and goes on
@@ -680,29 +699,48 @@ __global__ void __launch_bounds__(D * (P4 ? 4 : 8)) paged_merge_kernel(const __g
   const PagedAttentionArgs &a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int4 desc = __ldcg(p.desc + c);
-  const int n = desc.x;
+  const int4 desc = __ldcg(p.desc + 2 * c), where = __ldcg(p.desc + 2 * c + 1);
+  const int n = desc.x, nrows = desc.y, row0 = desc.z;
   if (n == 0) return;
   const float vs = __ldcg(p.v_unit);
   const int G = a.Hq / a.Hkv;
-  const Req req = load_req(a, desc.y, RT, p.faults);
-  const int row0 = desc.z * RT, nrows = min(RT, req.n * G - row0);
   // piece k's slot
   auto slot = [&](int k) { return p.slots + (size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * kMaxRows * (D + 2); };
+  const int i = tid / D, k = tid % D;
+  // the first pieces' sums are on their way while their factors are made
+  constexpr int N = 20;
+  float first[N];
+#pragma unroll
+  for (int x = 0; x < N; ++x) first[x] = x < n && i < nrows ? __ldcg(slot(x) + i * (D + 2) + k) : 0.f;
   if (warp < nrows) {
-    float m = -FLT_MAX;
-    for (int k = lane; k < n; k += 32) m = fmaxf(m, __ldcg(slot(k) + warp * (D + 2) + D));
+    float m = -FLT_MAX, mk = -FLT_MAX, lk = 0.f;
+    if (lane < n) {
+      mk = __ldcg(slot(lane) + warp * (D + 2) + D);
+      lk = __ldcg(slot(lane) + warp * (D + 2) + D + 1);
+    }
+    m = mk;
+    for (int x = lane + 32; x < n; x += 32) m = fmaxf(m, __ldcg(slot(x) + warp * (D + 2) + D));
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(dev::kFull, m, x));
+    const float e = exp2f(mk - m);
+    s_e[warp][lane] = e;
+    float l = e * lk;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(dev::kFull, l, x);
     if (lane == 0) {
       s_top[warp] = m;
-      s_l[warp] = 0.f;
+      s_l[warp] = l;
     }
   }
   __syncthreads();
-  const int i = tid / D, k = tid % D;
   float y = 0.f;
-  for (int k0 = 0; k0 < n; k0 += 32) {
+  if (i < nrows) {
+#pragma unroll
+    for (int x = 0; x < N; ++x) y = x < n ? fmaf(s_e[i][x], first[x], y) : y;
+    for (int x = N; x < min(n, 32); ++x) y = fmaf(s_e[i][x], __ldcg(slot(x) + i * (D + 2) + k), y);
+  }
+  for (int k0 = 32; k0 < n; k0 += 32) {  // only a grid of more SMs, or a unit of its own, has that many
+    __syncthreads();
     if (warp < nrows) {
       float e = 0.f, l = 0.f;
       if (k0 + lane < n) {
@@ -721,7 +759,6 @@ __global__ void __launch_bounds__(D * (P4 ? 4 : 8)) paged_merge_kernel(const __g
 #pragma unroll 8
       for (int x = 0; x < end; ++x) y = fmaf(s_e[i][x], __ldcg(slot(k0 + x) + i * (D + 2) + k), y);
     }
-    __syncthreads();
   }
   s_y[i][k] = y;
   __syncthreads();
@@ -730,7 +767,7 @@ __global__ void __launch_bounds__(D * (P4 ? 4 : 8)) paged_merge_kernel(const __g
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) v[e] = s_y[warp][place<D>(lane * (D / 32) + e)];
     const int qi = (row0 + warp) / G;
-    store_out<D>(a, (int64_t)req.q0 + qi, desc.w * G + (row0 + warp) - qi * G, lane, v, s_top[warp], s_l[warp],
+    store_out<D>(a, (int64_t)where.x + qi, desc.w * G + (row0 + warp) - qi * G, lane, v, s_top[warp], s_l[warp],
                  1.0f / (a.vq.sqrt_d * vs));
   }
 }
@@ -770,7 +807,7 @@ cudaError_t run_d(const RowsParams &p, bool p4, cudaStream_t s) {
 
 size_t paged_rows_workspace(int d) {
   const size_t ctas = decode_ctas();
-  return ctas * sizeof(int4) + 16 + 2 * ctas * kMaxRows * (d + 2) * sizeof(float);
+  return 2 * ctas * sizeof(int4) + 16 + 2 * ctas * kMaxRows * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_rows(const PagedAttentionArgs &a, cudaStream_t s) {
@@ -779,7 +816,7 @@ cudaError_t launch_paged_rows(const PagedAttentionArgs &a, cudaStream_t s) {
   const cudaError_t e = fault_word(&p.faults);
   if (e != cudaSuccess) return e;
   p.desc = static_cast<int4 *>(a.ws);
-  p.v_unit = reinterpret_cast<float *>(p.desc + decode_ctas());
+  p.v_unit = reinterpret_cast<float *>(p.desc + 2 * decode_ctas());
   p.slots = p.v_unit + 4;
   const bool p4 = (int64_t)a.max_q * (a.Hq / a.Hkv) <= 4;
   return a.kq.d == 64 ? run_d<64>(p, p4, s) : run_d<128>(p, p4, s);
