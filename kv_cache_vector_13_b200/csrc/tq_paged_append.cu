@@ -31,6 +31,21 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTokens = 4;  // tokens per block
 constexpr int E = 16;          // coordinates per lane
 
+// The values of a 16-byte word.
+template <int DT>
+__device__ __forceinline__ void widen(const uint4 &u, float *x) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == TQ_F32) {
+      x[i] = __uint_as_float(w[i]);
+    } else {
+      x[2 * i] = DT == TQ_BF16 ? dev::bf16lo(w[i]) : dev::f16lo(w[i]);
+      x[2 * i + 1] = DT == TQ_BF16 ? dev::bf16hi(w[i]) : dev::f16hi(w[i]);
+    }
+  }
+}
+
 struct AppendParams {
   PagedAppendArgs a;
   int tokens;          // tokens per block
@@ -62,7 +77,7 @@ __device__ __forceinline__ void store16(void *dst, int dt, const float (&v)[E]) 
 }
 
 template <int D, int DT>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendParams p) {
+__global__ void __launch_bounds__(kThreads, DT == TQ_F32 ? 2 : 3) paged_append_kernel(AppendParams p) {
   constexpr int T = D / E;           // lanes per row
   constexpr int RPW = 32 / T;        // rows per warp
   constexpr int ES = DT == TQ_F32 ? 4 : 2;
@@ -123,29 +138,62 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendParams p) 
 
   const int t = lane % T, rw = lane / T;
   const int groups = p.gq + 2 * p.gk;
-  for (int g = blockIdx.y * kWarps + warp; g < groups; g += gridDim.y * kWarps) {
-    const int kind = g < p.gq ? 0 : g < p.gq + p.gk ? 1 : 2;  // Q, K, V
-    const int H = kind == 0 ? a.Hq : a.Hkv;
-    int row = (g - (kind == 0 ? 0 : kind == 1 ? p.gq : p.gq + p.gk)) * RPW + rw;
-    const bool active = row < ntok * H;
-    if (!active) row = 0;  // idle lanes still take part in the shuffles
-    const int k = row / H, h = row - k * H;
-    const int64_t tok = tok0 + k;
+  // A group's rows: what kind, which token and head of the lane's row, and where that lies.
+  struct Group {
+    int kind, k, h;  // Q, K, V
+    bool active;
     const char *src;
-    if (kind == 0)
-      src = static_cast<const char *>(a.q) + (tok * a.q_st + h * a.q_sh) * ES;
-    else if (kind == 1)
-      src = static_cast<const char *>(a.k) + (tok * a.k_st + h * a.k_sh) * ES;
+  };
+  auto group = [&](int g) {
+    Group r;
+    r.kind = g < p.gq ? 0 : g < p.gq + p.gk ? 1 : 2;
+    const int H = r.kind == 0 ? a.Hq : a.Hkv;
+    int row = (g - (r.kind == 0 ? 0 : r.kind == 1 ? p.gq : p.gq + p.gk)) * RPW + rw;
+    r.active = row < ntok * H;
+    if (!r.active) row = 0;  // idle lanes still take part in the shuffles
+    r.k = (ntok > 1 && row >= H) + (ntok > 2 && row >= 2 * H) + (ntok > 3 && row >= 3 * H);
+    r.h = row - r.k * H;
+    const int64_t tok = tok0 + r.k;
+    if (r.kind == 0)
+      r.src = static_cast<const char *>(a.q) + (tok * a.q_st + r.h * a.q_sh) * ES;
+    else if (r.kind == 1)
+      r.src = static_cast<const char *>(a.k) + (tok * a.k_st + r.h * a.k_sh) * ES;
     else
-      src = static_cast<const char *>(a.v) + (tok * a.v_st + h * a.v_sh) * ES;
+      r.src = static_cast<const char *>(a.v) + (tok * a.v_st + r.h * a.v_sh) * ES;
+    return r;
+  };
+  constexpr int NR = E * ES / 16;  // 16-byte words of a lane
+  uint4 ahead[NR];
+  auto fetch = [&](const Group &r) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) ahead[i] = __ldg(reinterpret_cast<const uint4 *>(r.src + t * E * ES) + i);
+  };
+  const int step = gridDim.y * kWarps;
+  int g = blockIdx.y * kWarps + warp;
+  Group cur = group(min(g, groups - 1));
+  if (g < groups) fetch(cur);
+  for (; g < groups; g += step) {
+    const int kind = cur.kind, k = cur.k, h = cur.h;
+    const bool active = cur.active;
+    const char *src = cur.src;
+    const int64_t tok = tok0 + k;
     float x[E];
-    dev::load_block<DT, E>(src + t * E * ES, x);
+#pragma unroll
+    for (int i = 0; i < NR; ++i) widen<DT>(ahead[i], x + i * (16 / ES));
+    if (g + step < groups) {  // the next group's rows, while this one is worked on
+      cur = group(g + step);
+      fetch(cur);
+    }
 
     if (kind != 2 && t * E < a.rot_dim) {
       float y[E];  // each coordinate's partner
       if (a.adjacent) {
 #pragma unroll
         for (int i = 0; i < E; ++i) y[i] = x[i ^ 1];
+      } else if (a.rot_dim == D) {
+        // half a row away: the same coordinates of another lane
+#pragma unroll
+        for (int i = 0; i < E; ++i) y[i] = __shfl_xor_sync(dev::kFull, x[i], T / 2);
       } else {
         // half is a multiple of 8, so a chunk of 8 lies on one side of it
 #pragma unroll
@@ -203,6 +251,10 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendParams p) 
 
 struct ReadParams {
   PagedDequantArgs a;
+  dev::IndexSplit rows;    // row -> (token, head)
+  uint32_t page_mul;       // slot / page_size = (slot * page_mul) >> page_shift below 2^31 slots
+  int page_shift;
+  bool small;              // so many
   unsigned *faults;
 };
 
@@ -231,14 +283,14 @@ __global__ void __launch_bounds__(kThreads) paged_dequant_kernel(ReadParams p) {
     int64_t row = r0 + lane / T;
     const bool active = row < rows;
     if (!active) row = r0;
-    const int64_t tok = row / a.H;
-    const int h = (int)(row - tok * a.H);
+    int64_t none, tok, h;
+    dev::split_bhn(p.rows, row, none, tok, h);
     const int64_t slot = a.slots[tok];
     int64_t rec = -1;
     if (slot >= a.n_slots) {
       if (t == 0 && h == 0) atomicOr(p.faults, kFaultIndex);
     } else if (slot >= 0) {
-      const int64_t page = slot / a.page_size;
+      const int64_t page = p.small ? (int64_t)(((uint64_t)slot * p.page_mul) >> p.page_shift) : slot / a.page_size;
       rec = page * a.c.sb + (slot - page * a.page_size) * a.c.sn + h * a.c.sh;
     }
     float x[E], sc = 0.f;
@@ -296,7 +348,11 @@ cudaError_t launch_paged_append(const PagedAppendArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_paged_dequant(const PagedDequantArgs &a, cudaStream_t s) {
-  ReadParams p{a, nullptr};
+  ReadParams p{};
+  p.a = a;
+  p.rows = dev::make_index_split(a.T, a.H, a.T * a.H);
+  p.small = a.n_slots < ((int64_t)1 << 31);
+  dev::magic31_div(a.page_size, p.page_mul, p.page_shift);
   cudaError_t e = fault_word(&p.faults);
   if (e != cudaSuccess) return e;
   const int rpb = kWarps * (512 / a.q.d);
