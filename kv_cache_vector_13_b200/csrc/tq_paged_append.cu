@@ -31,6 +31,29 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTokens = 4;  // tokens per block
 constexpr int E = 16;          // coordinates per lane
 
+// The transform of tq_device.cuh with the same steps and roundings; a stage
+// across lanes is one multiply-add by +1 or -1 a pair (the product is exact),
+// without flipping a sign first.
+template <int T>
+__device__ __forceinline__ void fwht_row(float (&a)[E], int t) {
+#pragma unroll
+  for (int P = T / 2; P >= 1; P >>= 1) {
+    const float sign = t & P ? -1.f : 1.f;
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      const float o0 = __shfl_xor_sync(dev::kFull, a[i], P), o1 = __shfl_xor_sync(dev::kFull, a[i + 1], P);
+      dev::fma_x2(a[i], a[i + 1], a[i], a[i + 1], sign, sign, o0, o1);
+    }
+  }
+  dev::fwht_local<E>(a);
+}
+
+// The lane's signs of a rotation as +1 and -1.
+__device__ __forceinline__ void load_signs(const int8_t *signs, float (&s)[E]) {
+#pragma unroll
+  for (int i = 0; i < E; ++i) s[i] = signs[i] < 0 ? -1.f : 1.f;
+}
+
 // The values of a 16-byte word.
 template <int DT>
 __device__ __forceinline__ void widen(const uint4 &u, float *x) {
@@ -85,20 +108,17 @@ __global__ void __launch_bounds__(kThreads, DT == TQ_F32 ? 2 : 3) paged_append_k
   // float4 c * T + t, so the lanes of a row read consecutive 16-byte words
   __shared__ float4 s_cos[kMaxTokens][D / 4], s_sin[kMaxTokens][D / 4];
   __shared__ int64_t s_krec[kMaxTokens], s_vrec[kMaxTokens];  // record of head 0, or -1
-  __shared__ uint32_t s_sign[2][D / 32];
+  __shared__ float4 s_flip[2][D / 4];  // the rotations' signs, laid out alike
 
   const PagedAppendArgs &a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t tok0 = (int64_t)blockIdx.x * p.tokens;
   const int ntok = (int)min((int64_t)p.tokens, a.T - tok0);
 
-  if (warp < 2) {  // sign-flip masks, one ballot per 32 coordinates
-    const int8_t *signs = warp == 0 ? a.kq.signs : a.vq.signs;
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      const unsigned m = __ballot_sync(dev::kFull, signs[32 * w + lane] < 0);
-      if (lane == 0) s_sign[warp][w] = m;
-    }
+  for (int i = tid; i < 2 * D; i += kThreads) {
+    const int c = i % D;
+    const int8_t *signs = i < D ? a.kq.signs : a.vq.signs;
+    reinterpret_cast<float *>(&s_flip[i / D][((c % E) / 4) * T + c / E])[c & 3] = signs[c] < 0 ? -1.f : 1.f;
   }
   if (tid >= kThreads - kMaxTokens) {
     const int k = tid - (kThreads - kMaxTokens);
@@ -229,10 +249,13 @@ __global__ void __launch_bounds__(kThreads, DT == TQ_F32 ? 2 : 3) paged_append_k
     for (int m = 0; m < 7; ++m) P[m] = __float_as_uint(__ldg(q.thresholds + 8 + m));
     P[7] = 0;
     const float nrm = __fsqrt_rn(dev::fold_halves_sumsq<T, E>(x));
-    const uint32_t sw = s_sign[kind - 1][t * E / 32] >> ((t * E) & 31);
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = __uint_as_float(__float_as_uint(x[i]) ^ (((sw >> i) & 1u) << 31));
-    dev::fwht<T, E>(x, t);
+    for (int c = 0; c < E / 4; ++c) {
+      const float4 sg = s_flip[kind - 1][c * T + t];
+      dev::mul_x2(x[4 * c], x[4 * c + 1], x[4 * c], x[4 * c + 1], sg.x, sg.y);
+      dev::mul_x2(x[4 * c + 2], x[4 * c + 3], x[4 * c + 2], x[4 * c + 3], sg.z, sg.w);
+    }
+    fwht_row<T>(x, t);
     const float wsc = __fmul_rn(nrm, q.sqrt_d);
     const float inv = wsc > 0.0f ? __frcp_rn(wsc) : 0.0f;
     dev::scale_x2<E>(x, inv);
@@ -264,17 +287,11 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) paged_dequant_kernel(ReadParams p) {
   constexpr int T = D / E, RPW = 32 / T;
   __shared__ float s_cent[16];
-  __shared__ uint32_t s_sign[D / 32];
   const PagedDequantArgs &a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < 16) s_cent[tid] = a.q.centroids[tid];
-  if (warp == 1) {
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      const unsigned m = __ballot_sync(dev::kFull, a.q.signs[32 * w + lane] < 0);
-      if (lane == 0) s_sign[w] = m;
-    }
-  }
+  float sign[E];
+  load_signs(a.q.signs + (lane % T) * E, sign);
   __syncthreads();
   const int t = lane % T;
   const int64_t rows = a.T * a.H;
@@ -301,12 +318,11 @@ __global__ void __launch_bounds__(kThreads) paged_dequant_kernel(ReadParams p) {
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) x[i] = s_cent[dev::get_field<4>(W, i)];
-    dev::fwht<T, E>(x, t);
-    const uint32_t sw = s_sign[t * E / 32] >> ((t * E) & 31);
+    fwht_row<T>(x, t);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float y = __uint_as_float(__float_as_uint(x[i]) ^ (((sw >> i) & 1u) << 31));
-      x[i] = rec >= 0 ? y * sc : 0.f;
+    for (int i = 0; i < E; i += 2) {  // sc is 0 for a row without a record
+      dev::mul_x2(x[i], x[i + 1], x[i], x[i + 1], sign[i], sign[i + 1]);
+      dev::mul_x2(x[i], x[i + 1], x[i], x[i + 1], sc, sc);
     }
     if (active)
       store16(static_cast<char *>(a.out) + (row * D + t * E) * (a.out_dtype == TQ_F32 ? 4 : 2), a.out_dtype, x);
