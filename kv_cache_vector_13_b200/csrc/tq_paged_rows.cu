@@ -39,7 +39,8 @@ using namespace paged;
 constexpr int kStep = 32;                // tokens per step, in two halves of 16 that may lie in two pages
 constexpr uint32_t kTabAddr = 0x10000u;  // the pair tables: 64 KiB at this shared address
 constexpr uint32_t kPartAddr = 0x20000u; // the warps' partial sums
-constexpr int kMaxRows = 8;
+constexpr int kMaxRows = 8;               // query rows of a group of warps
+constexpr int kUnitRows = 32;             // of a unit: up to 4 groups
 constexpr int64_t kSteps = ((int64_t)1 << 42) - 1;
 constexpr int kStages = 2;               // a warp's steps in shared memory: one worked on, one on its way
 
@@ -63,13 +64,13 @@ template <int D>
 struct Low {
   int64_t base[Cfg<D>::kThreads];  // the line at each thread's first request
   int64_t warp[Cfg<D>::kWarps];
-  __half q[2][8][D + 8];           // operand columns: hi of each row, lo of each row
-  float f[kMaxRows];               // logit factor of each row
+  __half q[2][kUnitRows][D + 8];   // operand columns: hi of each row, lo of each row
+  float f[kUnitRows];              // logit factor of each row
   float m[Cfg<D>::kWarps][kMaxRows], l[Cfg<D>::kWarps][kMaxRows];
   float scale[2];                  // what the tables' values are to be divided by
   unsigned key[2];
   __half level[2][16];             // the scaled levels
-  float e[kMaxRows][Cfg<D>::kWarps], top[kMaxRows], sum[kMaxRows];  // merge of the warps
+  float e[Cfg<D>::kWarps][kMaxRows], top[kUnitRows], sum[kUnitRows];  // merge of the warps
 };
 
 template <int D>
@@ -80,7 +81,8 @@ __host__ __device__ constexpr uint32_t smem_end() {
 
 struct RowsParams {
   PagedAttentionArgs a;
-  float *slots;     // [2 * ctas][kMaxRows][D + 2]: sums, then M and L
+  int groups;       // warps are in so many groups of 4 or 8 query rows, which go through the same steps
+  float *slots;     // [2 * ctas][kUnitRows][D + 2]: sums, then M and L
   int4 *desc;       // [2 * ctas]: {pieces, rows, first row, head}, {first query row} of the unit that starts last in a range
   float *v_unit;    // what the values' table is to be divided by
   unsigned *faults;
@@ -183,11 +185,11 @@ __device__ __forceinline__ uint32_t v_place(int t, int c) {
 }
 
 // P4: up to 4 query rows a tile, hi and lo in one product; else up to 8.
-// UNIT: the tokens of a page lie side by side, and K and V records alike.
-template <int D, bool P4, bool UNIT>
+// MULTI: several groups of warps.  UNIT: the tokens of a page lie side by side, and K and V records alike.
+template <int D, bool P4, bool MULTI, bool UNIT>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr int W = Cfg<D>::kWarps, NT = Cfg<D>::kThreads, PITCH = Cfg<D>::kPitch;
-  constexpr int RT = P4 ? 4 : 8;  // query rows per tile
+  constexpr int RG = P4 ? 4 : 8;  // query rows per group
   constexpr int KS = D / 16;      // k steps of the scores
   constexpr int MV = D / 16;      // m tiles of the values
   constexpr int QS = P4 ? 1 : 2;  // products per step
@@ -204,6 +206,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
   const PagedAttentionArgs &a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
   const int G = a.Hq / a.Hkv, c = blockIdx.x;
+  const int groups = MULTI ? p.groups : 1;
+  const int RT = RG * groups, WG = W / groups;         // rows of a unit, warps of a group
+  const int group = MULTI ? warp / WG : 0, wg = warp - group * WG, gr = RG * group;  // the warp's group, place in it, first row
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const uint32_t dyn = (uint32_t)__cvta_generic_to_shared(s_raw);
   uint32_t dyn_bytes;
@@ -215,7 +220,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
     }
     return;
   }
-  float *parts = reinterpret_cast<float *>(s_raw + (kPartAddr - dyn));  // [W][RT][PITCH]
+  float *parts = reinterpret_cast<float *>(s_raw + (kPartAddr - dyn));  // [W][kMaxRows][PITCH]
 
   // ---- the tables' scales, and the line of steps: a run of requests a thread
   if (tid < 2) sm.key[tid] = 0xffffffffu;
@@ -311,12 +316,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
     const int nrows = min(RT, req.n * G - row0);
 
     const int32_t *row = a.table + (int64_t)r * a.table_stride;
-    const int n_steps = s1 - s0 > warp ? (s1 - s0 - warp + W - 1) / W : 0;
+    const int mine_rows = min(RG, nrows - gr);  // of the warp's group
+    const int n_steps = mine_rows > 0 && s1 - s0 > wg ? (s1 - s0 - wg + WG - 1) / WG : 0;
     // The records of 4 of the warp's steps, half lane % 2 of step it + lane / 2 % 4 a lane, found a batch ahead;
     // -1 without a page and behind the piece's last step.
     int64_t krec, vrec, krec2, vrec2;
     auto find = [&](int it, int64_t &kr, int64_t &vr) {
-      const int s = s0 + warp + (it + ((lane >> 1) & 3)) * W;
+      const int s = s0 + wg + (it + ((lane >> 1) & 3)) * WG;
       kr = vr = -1;
       const int t0 = s * kStep + 16 * (lane & 1);
       if (s < s1 && t0 < req.kv && t0 + 16 > req.first) {
@@ -412,7 +418,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
     for (int o = 0; o < QS; ++o)
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        const uint2 t = *reinterpret_cast<const uint2 *>(&s_q[o][g][q4 * (D / 4) + 4 * s]);
+        const uint2 t = *reinterpret_cast<const uint2 *>(&s_q[o][gr + g][q4 * (D / 4) + 4 * s]);
         qb[o][s][0] = t.x;
         qb[o][s][1] = t.y;
       }
@@ -421,20 +427,21 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
     float f[2], M[2], l[2];
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
-      const int i = (2 * q4 + o) & (RT - 1);
+      const int i = (2 * q4 + o) & (RG - 1);
       see_lo[o] = 0;
       see_hi[o] = INT_MAX;
-      if (i < nrows) {
-        const int pos = req.kv - req.n + (row0 + i) / G;
+      if (i < mine_rows) {
+        const int pos = req.kv - req.n + (row0 + gr + i) / G;
         see_hi[o] = a.causal ? max(pos + 1, 0) : req.kv;
         see_lo[o] = a.window > 0 ? max(pos + 1 - a.window, 0) : 0;
       }
-      f[o] = s_f[i];
+      f[o] = s_f[gr + i];
       M[o] = -FLT_MAX;
       l[o] = 0.f;
     }
-    // steps that every row of the tile sees whole
-    const int first_pos = req.kv - req.n + row0 / G, last_pos = req.kv - req.n + (row0 + nrows - 1) / G;
+    // steps that every row of the group sees whole
+    const int first_pos = req.kv - req.n + (row0 + gr) / G,
+              last_pos = req.kv - req.n + (row0 + gr + mine_rows - 1) / G;
     const int full_hi = a.causal ? max(first_pos + 1, 0) : req.kv;
     const int full_lo = a.window > 0 ? max(last_pos + 1 - a.window, 0) : 0;
 
@@ -496,7 +503,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
     };
 
     for (int it = 0; it < n_steps; ++it) {
-      const int t0 = (s0 + warp + it * W) * kStep;
+      const int t0 = (s0 + wg + it * WG) * kStep;
       const uint32_t halves = ok >> (2 * (it & 1)) & 3;
       const uint32_t from = ring + (it & 1) * Cfg<D>::kStepBytes;
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -599,7 +606,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
       float t = l[o];
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) t += __shfl_xor_sync(dev::kFull, t, x);
-      if (g == 0 && 2 * q4 < RT) {
+      if (g == 0 && 2 * q4 < RG) {
         s_m[warp][2 * q4 + o] = M[o];
         s_l[warp][2 * q4 + o] = t;
       }
@@ -613,37 +620,36 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
           x += __shfl_xor_sync(dev::kFull, x, 2);
           y += __shfl_xor_sync(dev::kFull, y, 2);
         }
-        if (2 * q4 < RT)
+        if (2 * q4 < RG)
           *reinterpret_cast<float2 *>(parts + ((size_t)warp * kMaxRows + 2 * q4 + o) * PITCH + 16 * j + 2 * g) =
               make_float2(x, y);
       }
     __syncthreads();
     const bool starts = s0 == req.lo, ends = s1 == req.hi;
-    // each warp's factor for each row
-    if (tid < W * RT) {
-      const int w = tid / RT, i = tid % RT;
-      float m = s_m[0][i];
-#pragma unroll
-      for (int x = 1; x < W; ++x) m = fmaxf(m, s_m[x][i]);
-      sm.e[i][w] = exp2f(s_m[w][i] - m);
-      if (w == 0) sm.top[i] = m;
+    // each warp's factor for each row of its group
+    if (tid < W * RG) {
+      const int w = tid / RG, i = tid % RG, w0 = MULTI ? w - w % WG : 0;
+      float m = s_m[w0][i];
+      for (int x = w0 + 1; x < w0 + WG; ++x) m = fmaxf(m, s_m[x][i]);
+      sm.e[w][i] = exp2f(s_m[w][i] - m);
+      if (w == w0) sm.top[RG * (w / WG) + i] = m;
     }
     __syncthreads();
-    float *slot = p.slots + (size_t)(2 * c + (starts ? 1 : 0)) * kMaxRows * (D + 2);
+    float *slot = p.slots + (size_t)(2 * c + (starts ? 1 : 0)) * kUnitRows * (D + 2);
     for (int u = tid; u < nrows * D; u += NT) {
-      const int i = u / D, k = u % D;  // place k of the row
+      const int i = u / D, k = u % D, w0 = MULTI ? i / RG * WG : 0, ri = i % RG;  // place k of the row
       float y = 0.f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) y = fmaf(sm.e[i][w], parts[(w * kMaxRows + i) * PITCH + k], y);
+      for (int w = w0; w < w0 + WG; ++w) y = fmaf(sm.e[w][ri], parts[(w * kMaxRows + ri) * PITCH + k], y);
       if (starts && ends)
-        parts[i * PITCH + k] = y;  // only this thread has read it
+        parts[(w0 * kMaxRows + ri) * PITCH + k] = y;  // only this thread has read it
       else
         slot[i * (D + 2) + k] = y;
     }
     if (tid < nrows) {
+      const int w0 = MULTI ? tid / RG * WG : 0, ri = tid % RG;
       float L = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) L = fmaf(sm.e[tid][w], s_l[w][tid], L);
+      for (int w = w0; w < w0 + WG; ++w) L = fmaf(sm.e[w][ri], s_l[w][ri], L);
       sm.sum[tid] = L;
       if (!(starts && ends)) {
         slot[tid * (D + 2) + D] = sm.top[tid];
@@ -653,9 +659,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
     if (starts && ends) {
       __syncthreads();
       for (int i = warp; i < nrows; i += W) {
+        const float *src = parts + (size_t)(i / RG * WG * kMaxRows + i % RG) * PITCH;
         float y[D / 32];
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) y[e] = parts[i * PITCH + place<D>(lane * (D / 32) + e)];
+        for (int e = 0; e < D / 32; ++e) y[e] = src[place<D>(lane * (D / 32) + e)];
         const int qi = (row0 + i) / G;
         store_out<D>(a, (int64_t)req.q0 + qi, h * G + (row0 + i) - qi * G, lane, y, sm.top[i], sm.sum[i], vscale);
       }
@@ -689,8 +696,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
 }
 
 // Merges the pieces of the unit that starts last in CTA c's range and goes on
-// behind it, in the order of the tokens: a block a unit, a coordinate of a row
-// a thread.
+// behind it, in the order of the tokens: a block a unit and group of rows, a
+// coordinate of a row a thread.
 template <int D, bool P4>
 __global__ void __launch_bounds__(D * (P4 ? 4 : 8)) paged_merge_kernel(const __grid_constant__ RowsParams p) {
   constexpr int RT = P4 ? 4 : 8;
@@ -700,12 +707,13 @@ __global__ void __launch_bounds__(D * (P4 ? 4 : 8)) paged_merge_kernel(const __g
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int4 desc = __ldcg(p.desc + 2 * c), where = __ldcg(p.desc + 2 * c + 1);
-  const int n = desc.x, nrows = desc.y, row0 = desc.z;
-  if (n == 0) return;
+  const int r8 = RT * blockIdx.y;  // the block's first row of the unit
+  const int n = desc.x, nrows = min(RT, desc.y - r8), row0 = desc.z + r8;
+  if (n == 0 || nrows <= 0) return;
   const float vs = __ldcg(p.v_unit);
   const int G = a.Hq / a.Hkv;
   // piece k's slot
-  auto slot = [&](int k) { return p.slots + (size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * kMaxRows * (D + 2); };
+  auto slot = [&](int k) { return p.slots + (size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * kUnitRows * (D + 2) + r8 * (D + 2); };
   const int i = tid / D, k = tid % D;
   // the first pieces' sums are on their way while their factors are made
   constexpr int N = 20;
@@ -772,11 +780,11 @@ __global__ void __launch_bounds__(D * (P4 ? 4 : 8)) paged_merge_kernel(const __g
   }
 }
 
-template <int D, bool P4, bool UNIT>
+template <int D, bool P4, bool MULTI, bool UNIT>
 cudaError_t run_rows(const RowsParams &p, cudaStream_t s) {
   // dynamic shared memory starts behind the 1 KiB that the system keeps
   const int dyn = (int)smem_end<D>() - 1024;
-  auto kern = paged_rows_kernel<D, P4, UNIT>;
+  auto kern = paged_rows_kernel<D, P4, MULTI, UNIT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
   if (e != cudaSuccess) return e;
   const int ctas = decode_ctas();
@@ -785,7 +793,7 @@ cudaError_t run_rows(const RowsParams &p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at{};
-  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)p.groups);
   cfg.blockDim = dim3(D * (P4 ? 4 : 8));
   cfg.stream = s;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -799,15 +807,16 @@ template <int D>
 cudaError_t run_d(const RowsParams &p, bool p4, cudaStream_t s) {
   const CacheView &k = p.a.k, &v = p.a.v;
   const bool unit = k.sn == 1 && v.sn == 1 && k.sb == v.sb && k.sh == v.sh;
-  if (p4) return unit ? run_rows<D, true, true>(p, s) : run_rows<D, true, false>(p, s);
-  return unit ? run_rows<D, false, true>(p, s) : run_rows<D, false, false>(p, s);
+  if (p4) return unit ? run_rows<D, true, false, true>(p, s) : run_rows<D, true, false, false>(p, s);
+  if (p.groups == 1) return unit ? run_rows<D, false, false, true>(p, s) : run_rows<D, false, false, false>(p, s);
+  return unit ? run_rows<D, false, true, true>(p, s) : run_rows<D, false, true, false>(p, s);
 }
 
 }  // namespace
 
 size_t paged_rows_workspace(int d) {
   const size_t ctas = decode_ctas();
-  return 2 * ctas * sizeof(int4) + 16 + 2 * ctas * kMaxRows * (d + 2) * sizeof(float);
+  return 2 * ctas * sizeof(int4) + 16 + 2 * ctas * kUnitRows * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_rows(const PagedAttentionArgs &a, cudaStream_t s) {
@@ -818,7 +827,10 @@ cudaError_t launch_paged_rows(const PagedAttentionArgs &a, cudaStream_t s) {
   p.desc = static_cast<int4 *>(a.ws);
   p.v_unit = reinterpret_cast<float *>(p.desc + 2 * decode_ctas());
   p.slots = p.v_unit + 4;
-  const bool p4 = (int64_t)a.max_q * (a.Hq / a.Hkv) <= 4;
+  // rows of a request and KV head that go through its tokens together; more of them are further units
+  const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv);
+  const bool p4 = rows <= 4;
+  p.groups = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
   return a.kq.d == 64 ? run_d<64>(p, p4, s) : run_d<128>(p, p4, s);
 }
 
