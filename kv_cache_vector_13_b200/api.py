@@ -5,7 +5,6 @@ of libtq_b200.so; torch supplies device memory, strides and the current
 stream.  The names follow the C ABI (include/tq.h).
 """
 
-import contextlib
 import ctypes
 import math
 from dataclasses import dataclass
@@ -359,15 +358,22 @@ def search_topk(qz: Quantizer, queries: torch.Tensor, db: PackedCache, k: int):
 
 # ------------------------------------------------------------ paged cache
 
-_NO_GUARD = contextlib.nullcontext()
+# the handle of a device's current stream, without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _on(device: int, stream=None):
-    """(guard, stream handle) of a call on tensors of this device."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    guard = _NO_GUARD if torch.cuda.current_device() == device else torch.cuda.device(device)
-    return guard, stream.cuda_stream
+def _call(device: int, stream, fn, *args) -> None:
+    """fn(*args, stream) with `device` current, on `stream` or that device's
+    current one."""
+    s = _raw_stream(device) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, s)
+    if status != L.TQ_OK:
+        L.check(status)
 
 
 def _strides(t: Optional[torch.Tensor]):
@@ -436,11 +442,9 @@ class PagePlanner:
         assert lens.shape == (R,) and new_lens.shape == (R,) and n_free.numel() == 1 and free_pages.dim() == 1
         _check(self.device, torch.int32, lens=lens, new_lens=new_lens, free_pages=free_pages, n_free=n_free)
         stride, width = _check_table(self.device, block_table, R)
-        guard, s = _on(self.device, stream)
-        with guard:
-            L.check(L.lib().tq_page_plan(
-                R, self.page_size, lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_pages.shape[0],
-                n_free.data_ptr(), block_table.data_ptr(), stride, width, self.max_tokens, *self._out, s))
+        _call(self.device, stream, L.lib().tq_page_plan, R, self.page_size, lens.data_ptr(), new_lens.data_ptr(),
+              free_pages.data_ptr(), free_pages.shape[0], n_free.data_ptr(), block_table.data_ptr(), stride, width,
+              self.max_tokens, *self._out)
         return p
 
 
@@ -512,12 +516,9 @@ def paged_append(kq: Quantizer, vq: Quantizer, k: torch.Tensor, v: torch.Tensor,
             q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
         assert q_out.shape == q.shape
         _check(dev, dt, q_out=q_out)
-    guard, s = _on(dev, stream)
-    with guard:
-        L.check(L.lib().tq_paged_append(
-            kq.c_ref(), vq.c_ref(), rp, pp, pos_stride, _DTYPES[dt], T, Hq, Hkv, _ptr(q), *_strides(q), k.data_ptr(),
-            *_strides(k), v.data_ptr(), *_strides(v), _ptr(q_out) if Hq else None, kcache.c_ref(), vcache.c_ref(),
-            n_pages, P, slots.data_ptr(), s))
+    _call(dev, stream, L.lib().tq_paged_append, kq.c_ref(), vq.c_ref(), rp, pp, pos_stride, _DTYPES[dt], T, Hq, Hkv,
+          _ptr(q), *_strides(q), k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), _ptr(q_out) if Hq else None,
+          kcache.c_ref(), vcache.c_ref(), n_pages, P, slots.data_ptr())
     return q_out if q is not None else None
 
 
@@ -533,10 +534,8 @@ def paged_dequant(qz: Quantizer, cache: PackedCache, slots: torch.Tensor, dtype=
         out = torch.empty((T, H, qz.d), dtype=dtype, device=cache.norms.device)
     assert out.shape == (T, H, qz.d) and out.dtype in _DTYPES
     _check(dev, out.dtype, out=out)
-    guard, s = _on(dev, stream)
-    with guard:
-        L.check(L.lib().tq_paged_dequant(qz.c_ref(), cache.c_ref(), n_pages, P, T, H, slots.data_ptr(),
-                                         _DTYPES[out.dtype], out.data_ptr(), s))
+    _call(dev, stream, L.lib().tq_paged_dequant, qz.c_ref(), cache.c_ref(), n_pages, P, T, H, slots.data_ptr(),
+          _DTYPES[out.dtype], out.data_ptr())
     return out
 
 
@@ -586,12 +585,10 @@ class PagedAttention:
         if lse is not None:
             assert lse.shape == (T, Hq)
             _check(dev, torch.float32, lse=lse)
-        guard, s = _on(dev, stream)
-        with guard:
-            L.check(L.lib().tq_paged_attention(
-                self.kq.c_ref(), self.vq.c_ref(), q.data_ptr(), _DTYPES[dt], T, Hq, Hkv, *_strides(q), kcache.c_ref(),
-                vcache.c_ref(), n_pages, P, block_table.data_ptr(), stride, R, width, kv_lens.data_ptr(), _ptr(cu_q),
-                max_q, scale, int(causal), window, out.data_ptr(), _ptr(lse), self._ws, self.ws_bytes, s))
+        _call(dev, stream, L.lib().tq_paged_attention, self.kq.c_ref(), self.vq.c_ref(), q.data_ptr(), _DTYPES[dt], T,
+              Hq, Hkv, *_strides(q), kcache.c_ref(), vcache.c_ref(), n_pages, P, block_table.data_ptr(), stride, R,
+              width, kv_lens.data_ptr(), _ptr(cu_q), max_q, scale, int(causal), window, out.data_ptr(), _ptr(lse),
+              self._ws, self.ws_bytes)
         return out
 
 
