@@ -59,6 +59,7 @@ struct TileParams {
   int page_shift;
   const __half *qhi, *qlo; // [T * Hq][D] turned rows
   const float *qf;         // [T * Hq] the factor their scores still need (softmax scale, log2 e, row scale)
+  int64_t max_tiles;       // that `line` has room for
   int32_t *first;          // [R + 1] first tile of each request
   int64_t *line;           // [tiles + 1] blocks (of one KV head) before each tile
   float *slots;            // [2 * ctas][rt * (D + 2)]
@@ -142,6 +143,12 @@ __global__ void __launch_bounds__(256) paged_tile_prep_kernel(const __grid_const
       const int64_t before = tiles + scan<256>(mine, s_warp, &all);
       if (r < a.R) p.first[r] = (int32_t)before;
       tiles += all;
+    }
+    if (tiles > p.max_tiles) {  // rows named twice by cu_q: more tiles than T rows have, and none is worked on
+      if (tid == 0) atomicOr(p.faults, kFaultIndex);
+      __syncthreads();
+      for (int r = tid; r < a.R; r += 256) p.first[r] = 0;
+      tiles = 0;
     }
     if (tid == 0) p.first[a.R] = (int32_t)tiles;
     __syncthreads();  // the block reads what it wrote
@@ -960,7 +967,7 @@ __global__ void __launch_bounds__(256) paged_tile_merge_kernel(const __grid_cons
 
 // Workspace: descriptors, slots, the line, turned rows and their factors.
 struct Layout {
-  size_t slots, first, line, qhi, qlo, qf, end;
+  size_t slots, first, line, tiles, qhi, qlo, qf, end;
 };
 
 Layout layout(int R, int64_t T, int Hq, int Hkv, int d) {
@@ -970,8 +977,8 @@ Layout layout(int R, int64_t T, int Hq, int Hkv, int d) {
   l.slots = up(ctas * sizeof(int4) + sizeof(float));
   l.first = up(l.slots + 2 * ctas * 256 * (d + 2) * sizeof(float));
   l.line = up(l.first + ((size_t)R + 1) * 4);
-  const size_t tiles = (size_t)T * (Hq / Hkv) / 128 + R + 1;  // at most, in tiles of 128 rows
-  l.qhi = up(l.line + tiles * 8);
+  l.tiles = (size_t)T * (Hq / Hkv) / 128 + R;  // at most, in tiles of 128 rows
+  l.qhi = up(l.line + (l.tiles + 1) * 8);
   l.qlo = up(l.qhi + (size_t)T * Hq * d * 2);
   l.qf = up(l.qlo + (size_t)T * Hq * d * 2);
   l.end = up(l.qf + (size_t)T * Hq * 4);
@@ -1031,6 +1038,7 @@ cudaError_t launch_paged_tile(const PagedAttentionArgs &a, cudaStream_t s) {
   p.v_unit = reinterpret_cast<float *>(p.desc + decode_ctas());
   p.slots = reinterpret_cast<float *>(w + l.slots);
   p.first = reinterpret_cast<int32_t *>(w + l.first);
+  p.max_tiles = (int64_t)l.tiles;
   p.line = reinterpret_cast<int64_t *>(w + l.line);
   p.qhi = reinterpret_cast<const __half *>(w + l.qhi);
   p.qlo = reinterpret_cast<const __half *>(w + l.qlo);

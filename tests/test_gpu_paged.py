@@ -600,6 +600,115 @@ def test_another_stream():
     assert torch.equal(a, ref) and torch.equal(b, ref)
 
 
+def test_many_requests():
+    # more requests than a block has threads, some without rows, some without tokens
+    rng = np.random.default_rng(1)
+    qs = rng.integers(0, 3, 900).tolist()
+    kv = rng.integers(0, 40, 900).tolist()
+    check_attention(paged_problem(19, qs, kv, 4, 2, 64, 16, torch.bfloat16))
+    qs = (rng.integers(0, 3, 600) * (rng.random(600) < 0.5)).tolist()
+    qs[7], kv = 40, rng.integers(0, 40, 600).tolist()
+    kv[7] = 50
+    check_attention(paged_problem(20, qs, kv, 4, 2, 64, 16, torch.float16))
+
+
+@pytest.mark.parametrize("G,qs", [(8, [2, 1, 2]), (8, [3, 3, 1]), (5, [6, 4, 2]), (16, [2, 1, 2]), (4, [1, 8, 9])])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_several_rows_a_head(G, qs, dtype):
+    # 16, 24, 32 and just above 32 rows of a request and KV head
+    p = paged_problem(G + sum(qs), qs, [300, 1030, 33], 2 * G, 2, 128, 16, dtype)
+    poison_unseen(p[3], p[4], p[5], p[6])
+    check_attention(p)
+    check_attention(p, window=70)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_fp16(d):
+    p = paged_problem(d, [140, 300, 2], [700, 300, 1000], 4, 2, d, 16, torch.float16)
+    poison_unseen(p[3], p[4], p[5], p[6])
+    check_attention(p)
+    check_attention(p, window=150)
+
+
+@pytest.mark.parametrize("qs", [[1, 1], [3, 60]])
+def test_a_nan_query_row_stays_alone(qs):
+    kq, vq, q, kc, vc, table, kv_lens, cu = paged_problem(21, qs, [200, 100], 8, 2, 128, 16, torch.bfloat16)
+    op = api.PagedAttention(kq, vq, 8, 2, 2, sum(qs), device=DEV)
+    ref = op(q, kc, vc, table, kv_lens, cu_q=cu, max_q=max(qs))
+    bad = q.clone()
+    bad[0, 1, 5] = float("nan")
+    bad[1, 6, 9] = float("inf")
+    out = op(bad, kc, vc, table, kv_lens, cu_q=cu, max_q=max(qs))
+    hit = torch.zeros(sum(qs), 8, dtype=torch.bool, device=DEV)
+    hit[0, 1] = hit[1, 6] = True
+    assert torch.equal(out[~hit], ref[~hit]) and bool(out[0, 1].isnan().all()) and not bool(out[1, 6].isfinite().any())
+
+
+@pytest.mark.parametrize("qs", [[1, 1, 1], [2, 70, 1]])
+def test_caches_beyond_32_bit_offsets(qs):
+    # 1.25 million pages of 64 records: code offsets pass 2^32 bytes, record offsets 2^26; the pages in use lie at
+    # both ends
+    kq, vq, q, kc, vc, table, kv_lens, cu = paged_problem(22, qs, [70, 130, 17], 8, 4, 128, 16, torch.bfloat16)
+    ref = api.PagedAttention(kq, vq, 8, 4, 3, sum(qs), device=DEV)(q, kc, vc, table, kv_lens, cu_q=cu, max_q=max(qs))
+    n, big = kc.norms.shape[0], 1_250_000
+    far = torch.arange(n, device=DEV)
+    far = torch.where(far % 2 == 0, far, big - 1 - far)
+    caches = []
+    for c, z in ((kc, kq), (vc, vq)):
+        b = api.empty_cache(z, big, 4, 16, device=DEV)
+        b.codes[far], b.norms[far] = c.codes, c.norms
+        caches.append(b)
+    t = torch.where(table >= 0, far[table.clamp(min=0).long()].int(), table)
+    out = api.PagedAttention(kq, vq, 8, 4, 3, sum(qs), device=DEV)(q, *caches, t, kv_lens, cu_q=cu, max_q=max(qs))
+    api.check()
+    assert torch.equal(out, ref)
+    slots = torch.tensor([big * 16 - 1, 5, big * 16 - 16], device=DEV)
+    k = torch.randn((3, 4, 128), device=DEV, generator=gen(23))
+    api.paged_append(kq, vq, k, k, *caches, slots)
+    x = api.paged_dequant(kq, caches[0], slots)
+    api.check()
+    small = api.empty_cache(kq, 1, 4, 16, device=DEV)
+    api.paged_append(kq, vq, k, k, small, api.empty_cache(vq, 1, 4, 16, device=DEV), torch.arange(3, device=DEV))
+    assert torch.equal(x, api.paged_dequant(kq, small, torch.arange(3, device=DEV)))
+
+
+def test_two_objects_on_two_streams():
+    ps = [paged_problem(30 + i, [1, 40], [900, 300 + i], 8, 2, 128, 16, torch.bfloat16) for i in range(2)]
+    ops = [api.PagedAttention(p[0], p[1], 8, 2, 2, 41, device=DEV) for p in ps]
+    run = lambda i, m: ops[i](ps[i][2][:m], *ps[i][3:6], ps[i][6], cu_q=torch.clamp(ps[i][7], max=m), max_q=m)  # noqa: E731
+    for m in (2, 41):  # the small tiles and the large ones
+        refs = [run(i, m) for i in range(2)]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        outs = [[], []]
+        for _ in range(10):
+            for i, s in enumerate(streams):
+                with torch.cuda.stream(s):
+                    outs[i].append(run(i, m))
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert all(torch.equal(o, refs[i]) for o in outs[i])
+
+
+def test_a_table_without_entries_and_rows_named_twice():
+    kq, vq, q, kc, vc, table, kv_lens, cu = paged_problem(24, [1, 60], [40, 70], 4, 2, 128, 16, torch.bfloat16)
+    op = api.PagedAttention(kq, vq, 4, 2, 2, 61, device=DEV)
+    for m in (1, 60):
+        out = op(q, kc, vc, table[:, :0], kv_lens, cu_q=cu, max_q=m)
+        with pytest.raises(L.TqError):
+            api.check()
+        assert bool((out == 0).all())
+    many = torch.tensor([0, 61] * 40 + [0], dtype=torch.int32, device=DEV)  # 40 times the same rows
+    t, lens = table[:1].repeat(80, 1), kv_lens[:1].repeat(80)
+    big = api.PagedAttention(kq, vq, 4, 2, 80, 61, device=DEV)
+    big(q, kc, vc, t, lens, cu_q=many, max_q=61)
+    try:
+        api.check()
+    except L.TqError:
+        pass
+    api.check()
+
+
 # ------------------------------------------------------------ a serving loop
 
 @pytest.mark.parametrize("d,Hq,Hkv,P", [(128, 8, 2, 16), (64, 6, 3, 32)])
