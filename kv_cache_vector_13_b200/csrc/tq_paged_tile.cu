@@ -62,7 +62,7 @@ struct TileParams {
   int64_t max_tiles;       // that `line` has room for
   int32_t *first;          // [R + 1] first tile of each request
   int64_t *line;           // [tiles + 1] blocks (of one KV head) before each tile
-  float *slots;            // [2 * ctas][rt * (D + 2)]
+  float *slots;            // [2 * ctas][rt][D + 4]: a row's sums, then M and L
   int4 *desc;              // [ctas]
   float *v_unit;           // what the values' table is to be divided by
   unsigned *faults;
@@ -867,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
       }
       if (x == 0 || (!SPLIT && both)) {
         const bool done = q.starts && q.ends;
-        float *slot = p.slots + (size_t)(2 * c + (q.starts ? 1 : 0)) * RT * (D + 2);
+        float *slot = p.slots + (size_t)(2 * c + (q.starts ? 1 : 0)) * RT * (D + 4) + (size_t)i * (D + 4);
         const float inv = 1.0f / (l * a.vq.sqrt_d * sm.scale[1]);
         float y[D];
 #pragma unroll
@@ -887,10 +887,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         if (!done && live) {
 #pragma unroll
           for (int e = 0; e < D; e += 4)
-            *reinterpret_cast<float4 *>(slot + ((size_t)(e / 4) * RT + i) * 4) =
-                make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-          slot[(size_t)D * RT + i] = M;
-          slot[(size_t)(D + 1) * RT + i] = l;
+            *reinterpret_cast<float4 *>(slot + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          *reinterpret_cast<float2 *>(slot + D) = make_float2(M, l);
         }
         if (done && live) {  // inverse rotation of the thread's row
           dev::fwht_local<D>(y);
@@ -928,41 +926,52 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
 }
 
 // Merges the pieces of the unit that starts last in CTA c's range and goes on
-// behind it, in the order of the tokens: 32 rows a block, a warp a row at a time.
+// behind it, in the order of the tokens: a warp a row.
 template <int D>
 __global__ void __launch_bounds__(256) paged_tile_merge_kernel(const __grid_constant__ TileParams p) {
   const PagedAttentionArgs &a = p.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x, RT = p.rt;
+  const int lane = threadIdx.x & 31, i = 8 * blockIdx.y + (threadIdx.x >> 5), c = blockIdx.x, RT = p.rt;
+  constexpr int C = D / 32;  // coordinates a lane
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int4 desc = __ldcg(p.desc + c);
-  if (desc.x == 0) return;
+  const int n = desc.x;
+  if (n == 0) return;
   const float vs = __ldcg(p.v_unit);
   const int G = a.Hq / a.Hkv;
   const Req req = load_req(a, desc.y, p.faults);
-  const int row0 = desc.z * RT, nrows = min(RT, req.n * G - row0);
-  auto slot = [&](int k) { return p.slots + (size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * RT * (D + 2); };
-  for (int i = 32 * blockIdx.y + warp; i < min(nrows, 32 * (int)blockIdx.y + 32); i += 8) {
-    float m = -FLT_MAX;
-    for (int k = lane; k < desc.x; k += 32) m = fmaxf(m, __ldcg(slot(k) + (size_t)D * RT + i));
+  const int row0 = desc.z * RT;
+  if (i >= min(RT, req.n * G - row0)) return;
+  auto slot = [&](int k) { return p.slots + ((size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * RT + i) * (D + 4); };
+  float m = -FLT_MAX;
+  for (int k = lane; k < n; k += 32) m = fmaxf(m, __ldcg(slot(k) + D));
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(dev::kFull, m, x));
-    float L = 0.f, y[D / 32];
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(dev::kFull, m, x));
+  float L = 0.f, y[C];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) y[e] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < desc.x; ++k) {
-      const float *s = slot(k);
-      const float f = exp2f(__ldcg(s + (size_t)D * RT + i) - m);
-      L = fmaf(f, __ldcg(s + (size_t)(D + 1) * RT + i), L);
+  for (int e = 0; e < C; ++e) y[e] = 0.f;
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    float f = 0.f;
+    if (k0 + lane < n) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2 *>(slot(k0 + lane) + D));
+      f = exp2f(ml.x - m);
+      L = fmaf(f, ml.y, L);
+    }
+    const int end = min(32, n - k0);
+#pragma unroll 8
+    for (int k = 0; k < end; ++k) {
+      const float fk = __shfl_sync(dev::kFull, f, k), *s = slot(k0 + k) + lane * C;
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) {
-        const int d = lane * (D / 32) + e;
-        y[e] = fmaf(f, __ldcg(s + ((size_t)(d >> 2) * RT + i) * 4 + (d & 3)), y[e]);
+      for (int e = 0; e < C; e += 2) {
+        const float2 v = __ldcg(reinterpret_cast<const float2 *>(s + e));
+        y[e] = fmaf(fk, v.x, y[e]);
+        y[e + 1] = fmaf(fk, v.y, y[e + 1]);
       }
     }
-    const int qi = (row0 + i) / G;
-    store_out<D>(a, (int64_t)req.q0 + qi, desc.w * G + (row0 + i) - qi * G, lane, y, m, L, 1.0f / (a.vq.sqrt_d * vs));
   }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(dev::kFull, L, x);
+  const int qi = (row0 + i) / G;
+  store_out<D>(a, (int64_t)req.q0 + qi, desc.w * G + (row0 + i) - qi * G, lane, y, m, L, 1.0f / (a.vq.sqrt_d * vs));
 }
 
 // Workspace: descriptors, slots, the line, turned rows and their factors.
@@ -975,7 +984,7 @@ Layout layout(int R, int64_t T, int Hq, int Hkv, int d) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   Layout l;
   l.slots = up(ctas * sizeof(int4) + sizeof(float));
-  l.first = up(l.slots + 2 * ctas * 256 * (d + 2) * sizeof(float));
+  l.first = up(l.slots + 2 * ctas * 256 * (d + 4) * sizeof(float));
   l.line = up(l.first + ((size_t)R + 1) * 4);
   l.tiles = (size_t)T * (Hq / Hkv) / 128 + R;  // at most, in tiles of 128 rows
   l.qhi = up(l.line + (l.tiles + 1) * 8);
@@ -1008,7 +1017,7 @@ cudaError_t run_tile(const TileParams &p, cudaStream_t s) {
   cfg.dynamicSmemBytes = (size_t)dyn;
   e = cudaLaunchKernelEx(&cfg, paged_tile_kernel<D, SPLIT, HL>, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(p.rt / 32));
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(p.rt / 8));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_tile_merge_kernel<D>, p);
