@@ -18,6 +18,13 @@
 // on in fp32, so positions up to 2^31 keep their phase.
 // A pair's other half comes from the row itself through L1 when it lies in
 // another lane (pairs half a head apart).
+//
+// Both kernels are bound by the shared-memory pipe, which does the shuffles too:
+// 48 of them per four rows of 128 for the transform's stages across lanes; 72%
+// of its rate in the read-back.  A row in two lanes (64 coordinates each) needs
+// a third of the shuffles but scatters the loads: 66 us against 61 (read-back of
+// 65536 rows of 8 heads, 2.8 TB/s), 218 against 163 (append of 16384 tokens, 32
+// / 8 heads, and its two read-backs).
 
 #include "../../include/tq.h"
 #include "tq_device.cuh"

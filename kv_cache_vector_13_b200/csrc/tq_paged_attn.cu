@@ -201,7 +201,7 @@ size_t paged_attention_workspace(int R, int64_t T, int Hq, int Hkv, int d) {
 cudaError_t launch_paged_attention(const PagedAttentionArgs &a, cudaStream_t s) {
   // Query rows of a request and KV head.  The small tiles decode the cache once for 8 rows, the large ones for 128 or
   // 256, with more work around each block: 64 requests of up to 4001 tokens, 64 / 8 heads, us, small and large tiles:
-  // 16 rows 210 and 348; 32 rows 327 and 365 (bf16), 326 and 483 (fp16); at 64 rows twice the first against the same.
+  // 16 rows 173 and 303 (bf16), 174 and 424 (fp16); 32 rows 243 and 308, 243 and 435; 64 rows 481 and 313, 481 and 436.
   const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv);
   if (a.kq.d != 256) return rows <= 32 ? launch_paged_rows(a, s) : launch_paged_tile(a, s);
   GeneralParams p{a, nullptr};

@@ -15,6 +15,10 @@
 // writes the page's block-table entry; a page's id is read from the free list
 // itself by every token of a new page, and from the table only for pages that
 // were there before, so no thread reads an entry that another one writes.
+//
+// Bound by its launch and the chain of loads, scan and search, not by bytes:
+// 16 requests 5.1 us, 257 requests 6.5 us, 2048 requests with new prompts (5 MB
+// in and out) 14.4 us.
 
 #include "tq_paged.h"
 

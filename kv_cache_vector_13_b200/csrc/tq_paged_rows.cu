@@ -1,7 +1,7 @@
 // Attention of a few query rows a request over a paged 4-bit cache (sm_100a):
 // decode, and the verification of a few draft tokens.
 //
-// Work: a unit is (request, KV head, tile of query rows), a step 16 cached
+// Work: a unit is (request, KV head, tile of query rows), a step 32 cached
 // tokens.  All units' steps form one line, cut into equal ranges, one a CTA
 // (one persistent CTA an SM), so requests of any lengths balance; a CTA's
 // part of a unit is a piece, whose steps its warps take in turn.  Units cut by
@@ -21,6 +21,23 @@
 // at one coordinate.  The order of coordinates within the products is free, so
 // every lane loads whole 16-byte (K) and 8-byte (V) runs of a record.  Norms
 // enter behind the products: ||k|| scales the logit, ||v|| the weight.
+//
+// Up to 8 rows a group: a unit of more has groups of warps, each with 8 of the
+// rows, which go through the same steps together, so a record comes from
+// memory once (128 requests of 4 rows, 64 / 8 heads: 502 us as units of 8
+// rows, 404 us with groups).
+//
+// A step's records come through a ring of two stages in shared memory a warp
+// (cp.async): the next step's are on their way while one is worked on (4
+// requests of up to 262144 tokens 206 us, against 265 with a single and 296
+// with a double buffer in registers).
+//
+// Bound by the instruction stream, 332 warp instructions per 16 tokens of a KV
+// head (128 of them the byte permutes and table reads) at 53% of the issue
+// slots.  Measured on a B200, d = 128: 16 requests of up to 65536 tokens
+// (551 MB), 32 / 8 heads, bf16, 195 us, 2.8 TB/s; 1 x 32768 tokens 23.5 us, of
+// which 11.5 are left with a single step; 128 requests of 4 rows and up to 4001
+// tokens, 64 / 8 heads, fp16, 404 us.
 
 #include "../../include/tq.h"
 #include "tq_device.cuh"
@@ -46,10 +63,7 @@ constexpr int kStages = 2;               // a warp's steps in shared memory: one
 
 template <int D>
 struct Cfg {
-#ifndef RW
-#define RW 12
-#endif
-  static constexpr int kWarps = RW;
+  static constexpr int kWarps = 12;  // 168 registers a thread; 16 warps of 128 took 207 us where 12 take 198
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kPitch = D + 4;  // floats of a partial row (no bank clash between rows)
   // a step: K codes, V codes, norms of each

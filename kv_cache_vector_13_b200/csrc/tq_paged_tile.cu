@@ -26,6 +26,12 @@
 //   split: 128 rows a tile, even blocks to one set, odd ones to the other,
 //          which are merged at the end (few rows a unit); with HL the rows and
 //          weights are fp16 pairs hi + lo, two products each (fp16 outputs).
+//
+// Bound by the chain from a block's scores through the softmax and the weights
+// to its values' product, two sets deep: a softmax takes 2.4 to 3.5 thousand
+// cycles, the products about 2 thousand.  Measured on a B200, bf16, 32 / 8
+// heads, d = 128: 3 requests of 2048 rows on up to 16384 tokens, causal (920
+// GFLOP), 1499 us, 614 TFLOP/s; 2048 rows on 8192 tokens 419 us.
 
 #include "../../include/tq.h"
 #include "tq_device.cuh"
@@ -670,10 +676,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         if (last) umma::commit(bar(sm.o_fin[x]));
       };
       const int mine = x < (both ? 2 : 1) ? (SPLIT ? (both ? (nblk + 1 - x) / 2 : nblk) : nblk) : 0;
-      // The sets take turns at the softmax, one's products meanwhile: left alone they fall into step, and the
-      // tensor cores and the other pipes idle in turn.  Barrier 4 lets the even set go on, 5 the odd one.
-      const int turns[2] = {mine, both ? (SPLIT ? (x == 0 ? nblk / 2 : (nblk + 1) / 2) : nblk) : 0};  // mine, the other's
-      if (both && x == 1) asm volatile("bar.arrive 4, 256;" ::: "memory");
       if (mine > 0 && issuer) scores(block(0));
       __syncwarp();
       for (int k = 0; k < mine; ++k) {
@@ -683,10 +685,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         wait(sm.n_full[nb], u / kNormBufs);
         wait(sm.s_full[x], items_done[x] + k);
         umma::fence_after();
-        if (both) {
-          if (x == 0) asm volatile("bar.sync 4, 256;" ::: "memory");
-          else asm volatile("bar.sync 5, 256;" ::: "memory");
-        }
         const uint4 vm = *reinterpret_cast<const uint4 *>(sm.valid[nb]);
         const uint32_t valid[4] = {vm.x, vm.y, vm.z, vm.w};
         const bool whole = see_lo <= j0 && see_hi >= j0 + kBlk && (vm.x & vm.y & vm.z & vm.w) == ~0u;
@@ -827,10 +825,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         if (__any_sync(dev::kFull, live)) {
           if (__all_sync(dev::kFull, whole || !live)) item(std::false_type{});
           else item(std::true_type{});
-        }
-        if (both) {  // the other set's turn, if it has another
-          if (x == 0 && k < turns[1]) asm volatile("bar.arrive 5, 256;" ::: "memory");
-          if (x == 1 && k + 1 < turns[1]) asm volatile("bar.arrive 4, 256;" ::: "memory");
         }
         wait_st();
         umma::fence_before();
