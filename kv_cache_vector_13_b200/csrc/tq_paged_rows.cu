@@ -56,8 +56,8 @@ using namespace paged;
 constexpr int kStep = 32;                // tokens per step, in two halves of 16 that may lie in two pages
 constexpr uint32_t kTabAddr = 0x10000u;  // the pair tables: 64 KiB at this shared address
 constexpr uint32_t kPartAddr = 0x20000u; // the warps' partial sums
-constexpr int kMaxRows = 8;               // query rows of a group of warps
-constexpr int kUnitRows = 32;             // of a unit: up to 4 groups
+constexpr int kMaxRows = 16;              // query rows of a group of warps
+constexpr int kUnitRows = 32;             // of a unit: up to 2 groups
 constexpr int64_t kSteps = ((int64_t)1 << 42) - 1;
 constexpr int kStages = 2;               // a warp's steps in shared memory: one worked on, one on its way
 
@@ -78,8 +78,9 @@ template <int D>
 struct Low {
   int64_t base[Cfg<D>::kThreads];  // the line at each thread's first request
   int64_t warp[Cfg<D>::kWarps];
-  __half q[2][kUnitRows][D + 8];   // operand columns: hi of each row, lo of each row
-  float f[kUnitRows];              // logit factor of each row
+  alignas(16) __half q[2][kUnitRows][D + 32];  // operand columns: hi of each row, lo of each row (q_place)
+  float f[kUnitRows];                          // logit factor of each row
+  int see_lo[kUnitRows], see_hi[kUnitRows];    // the tokens that each row sees
   float m[Cfg<D>::kWarps][kMaxRows], l[Cfg<D>::kWarps][kMaxRows];
   float scale[2];                  // what the tables' values are to be divided by
   unsigned key[2];
@@ -95,7 +96,7 @@ __host__ __device__ constexpr uint32_t smem_end() {
 
 struct RowsParams {
   PagedAttentionArgs a;
-  int groups;       // warps are in so many groups of 4 or 8 query rows, which go through the same steps
+  int groups;       // warps are in so many groups of 4, 8 or 16 query rows, which go through the same steps
   float *slots;     // [2 * ctas][kUnitRows][D + 2]: sums, then M and L
   int4 *desc;       // [2 * ctas]: {pieces, rows, first row, head}, {first query row} of the unit that starts last in a range
   float *v_unit;    // what the values' table is to be divided by
@@ -198,15 +199,25 @@ __device__ __forceinline__ uint32_t v_place(int t, int c) {
   return (uint32_t)((t ^ ((t >> 2) & 1)) * (D / 2) + (D == 128 ? (c ^ (((t >> 1) & 1) << 1)) * 16 : c * 16));
 }
 
-// P4: up to 4 query rows a tile, hi and lo in one product; else up to 8.
+// Where coordinate k of a query row lies: a lane's words of two k steps are 16
+// bytes, and a quarter-warp's fall into different banks.
+template <int D>
+__device__ __forceinline__ int q_place(int k) {
+  const int u = k % (D / 4);
+  return 8 * (4 * (u / 8) + k / (D / 4)) + u % 8;
+}
+
+// RG: query rows of a group of warps.  Up to 4: hi and lo are columns of one
+// product; 8: one column tile; 16: two, for which a warp reads the tables once.
 // MULTI: several groups of warps.  UNIT: the tokens of a page lie side by side, and K and V records alike.
-template <int D, bool P4, bool MULTI, bool UNIT>
+template <int D, int RG, bool MULTI, bool UNIT, bool HL>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr int W = Cfg<D>::kWarps, NT = Cfg<D>::kThreads, PITCH = Cfg<D>::kPitch;
-  constexpr int RG = P4 ? 4 : 8;  // query rows per group
+  constexpr bool P4 = RG == 4;
+  constexpr int NC = RG == 16 ? 2 : 1;  // column tiles
   constexpr int KS = D / 16;      // k steps of the scores
   constexpr int MV = D / 16;      // m tiles of the values
-  constexpr int QS = P4 ? 1 : 2;  // products per step
+  constexpr int QS = HL && !P4 ? 2 : 1;  // products per step
   extern __shared__ __align__(16) unsigned char s_raw[];
   Low<D> &sm = *reinterpret_cast<Low<D> *>(s_raw);
   auto &s_base = sm.base;
@@ -417,73 +428,86 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
       }
       dev::fwht<32, D / 32>(v, lane);
       const float f = row_scale<D / 32>(v);
-      if (lane == 0) s_f[i] = kscale / f;
+      if (lane == 0) {
+        // a row that is not there sees everything (and goes nowhere)
+        int lo = 0, hi = INT_MAX;
+        if (i < nrows) {
+          const int pos = req.kv - req.n + (row0 + i) / G;
+          hi = a.causal ? max(pos + 1, 0) : req.kv;
+          lo = a.window > 0 ? max(pos + 1 - a.window, 0) : 0;
+        }
+        s_f[i] = kscale / f;
+        sm.see_lo[i] = lo;
+        sm.see_hi[i] = hi;
+      }
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) {
         const float y = v[e] * f;
         const __half hi = __float2half_rn(y);
-        s_q[0][i][lane * (D / 32) + e] = hi;
-        s_q[P4 ? 0 : 1][P4 ? i + 4 : i][lane * (D / 32) + e] = __float2half_rn(y - __half2float(hi));
+        const int k = q_place<D>(lane * (D / 32) + e);
+        s_q[0][i][k] = hi;
+        if (HL) s_q[P4 ? 0 : 1][P4 ? i + 4 : i][k] = __float2half_rn(y - __half2float(hi));
       }
     }
     __syncthreads();
-    uint32_t qb[QS][KS][2];
+    // the query operands of k steps 2 w and 2 w + 1: kept in registers for one column tile
+    uint4 qb[NC == 1 ? QS : 1][NC == 1 ? KS / 2 : 1];
+    auto load_q = [&](int o, int ct, int w) {
+      return *reinterpret_cast<const uint4 *>(&s_q[o][gr + 8 * ct + g][8 * (4 * w + q4)]);
+    };
+    if constexpr (NC == 1) {
 #pragma unroll
-    for (int o = 0; o < QS; ++o)
+      for (int o = 0; o < QS; ++o)
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const uint2 t = *reinterpret_cast<const uint2 *>(&s_q[o][gr + g][q4 * (D / 4) + 4 * s]);
-        qb[o][s][0] = t.x;
-        qb[o][s][1] = t.y;
-      }
-    // the lane's two rows; one that is not there sees everything (and goes nowhere)
-    int see_lo[2], see_hi[2];
-    float f[2], M[2], l[2];
-#pragma unroll
-    for (int o = 0; o < 2; ++o) {
-      const int i = (2 * q4 + o) & (RG - 1);
-      see_lo[o] = 0;
-      see_hi[o] = INT_MAX;
-      if (i < mine_rows) {
-        const int pos = req.kv - req.n + (row0 + gr + i) / G;
-        see_hi[o] = a.causal ? max(pos + 1, 0) : req.kv;
-        see_lo[o] = a.window > 0 ? max(pos + 1 - a.window, 0) : 0;
-      }
-      f[o] = s_f[gr + i];
-      M[o] = -FLT_MAX;
-      l[o] = 0.f;
+        for (int w = 0; w < KS / 2; ++w) qb[o][w] = load_q(o, 0, w);
     }
+    // the lane's rows, two a column tile
+    auto row_of = [&](int ct, int o) { return gr + 8 * ct + ((2 * q4 + o) & (RG < 8 ? RG - 1 : 7)); };
+    float f[NC][2], M[NC][2], l[NC][2];
+#pragma unroll
+    for (int ct = 0; ct < NC; ++ct)
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        f[ct][o] = s_f[row_of(ct, o)];
+        M[ct][o] = -FLT_MAX;
+        l[ct][o] = 0.f;
+      }
     // steps that every row of the group sees whole
     const int first_pos = req.kv - req.n + (row0 + gr) / G,
               last_pos = req.kv - req.n + (row0 + gr + mine_rows - 1) / G;
     const int full_hi = a.causal ? max(first_pos + 1, 0) : req.kv;
     const int full_lo = a.window > 0 ? max(last_pos + 1 - a.window, 0) : 0;
 
-    float acc[MV][4];
+    float acc[NC][MV][4];
 #pragma unroll
-    for (int j = 0; j < MV; ++j)
+    for (int ct = 0; ct < NC; ++ct)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+      for (int j = 0; j < MV; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[ct][j][e] = 0.f;
 
     // The running softmax of the lane's rows over its tokens 8 i + g (value [i][o]: row o): scores in, weights
     // times value norms out.  M is a reference that moves only when one of them would pass 2^14 (fp16 ends at 2^16).
-    auto soft = [&](auto edge, int t0, uint32_t halves, float (&t)[4][2], const float (&kn)[4], const float (&vn)[4]) {
+    auto soft = [&](auto edge, auto tile, int t0, uint32_t halves, float (&t)[4][2], const float (&kn)[4],
+                    const float (&vn)[4], const float (&lv)[4]) {
       constexpr bool EDGE = decltype(edge)::value;
-      float lv[4], s[4][2], mx = -INFINITY;
+      constexpr int CT = decltype(tile)::value;
+      float s[4][2], mx = -INFINITY;
       bool seen[4][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = t0 + 8 * i + g;
-        lv[i] = fmaxf(log2_approx(vn[i]), -64.f);
+      for (int o = 0; o < 2; ++o) {
+        const int lo = EDGE ? sm.see_lo[row_of(CT, o)] : 0, hi = EDGE ? min(sm.see_hi[row_of(CT, o)], req.kv) : 0;
 #pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          seen[i][o] = !EDGE || (j >= see_lo[o] && j < see_hi[o] && j < req.kv && (halves >> (i >> 1) & 1));
-          s[i][o] = t[i][o] * (f[o] * kn[i]);
-          t[i][o] = s[i][o] - M[o];
+        for (int i = 0; i < 4; ++i) {
+          const int j = t0 + 8 * i + g;
+          seen[i][o] = !EDGE || (j >= lo && j < hi && (halves >> (i >> 1) & 1));
+          s[i][o] = t[i][o] * (f[CT][o] * kn[i]);
+          t[i][o] = s[i][o] - M[CT][o];
           if (EDGE && !seen[i][o]) t[i][o] = -INFINITY;
         }
-        mx = fmaxf(mx, fmaxf(t[i][0], t[i][1]) + lv[i]);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(t[i][0], t[i][1]) + lv[i]);
       if (__any_sync(dev::kFull, mx > 14.f)) {
         float r2[2];
 #pragma unroll
@@ -493,24 +517,24 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
           for (int i = 0; i < 4; ++i) m = fmaxf(m, seen[i][o] ? s[i][o] + lv[i] : -INFINITY);
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(dev::kFull, m, x));
-          m = fmaxf(M[o], m);
-          r2[o] = exp2f(M[o] - m);
-          M[o] = m;
-          l[o] *= r2[o];
+          m = fmaxf(M[CT][o], m);
+          r2[o] = exp2f(M[CT][o] - m);
+          M[CT][o] = m;
+          l[CT][o] *= r2[o];
 #pragma unroll
           for (int i = 0; i < 4; ++i) t[i][o] = seen[i][o] ? s[i][o] - m : -INFINITY;
         }
 #pragma unroll
         for (int j = 0; j < MV; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[j][e] *= r2[e & 1];
+          for (int e = 0; e < 4; ++e) acc[CT][j][e] *= r2[e & 1];
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
           t[i][o] = exp2_approx(t[i][o]);
-          l[o] += t[i][o];
+          l[CT][o] += t[i][o];
           t[i][o] *= vn[i];
           if (EDGE && !seen[i][o]) t[i][o] = 0.f;
         }
@@ -530,58 +554,88 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
       issue(it + 1);  // into the stage of step it - 1
       if (!halves) continue;
       // ---- scores: value 2 x + o of half i is token 16 i + 8 x + g, column 2 q4 + o
-      float sc[2][4];
+      float sc[NC][2][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int ct = 0; ct < NC; ++ct)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[i][e] = 0.f;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t c0[D / 32], c1[D / 32];  // codes of tokens 16 i + g and 16 i + 8 + g
-        lds_words(from + (16 * i + g) * (D / 2) + q4 * (D / 8), c0);
-        lds_words(from + (16 * i + 8 + g) * (D / 2) + q4 * (D / 8), c1);
+          for (int e = 0; e < 4; ++e) sc[ct][i][e] = 0.f;
+      // a query operand that is not kept is read once for both halves, so their codes come in runs of two words
+      constexpr int CW = NC == 1 ? D / 32 : 2, HV = NC == 1 ? 1 : 2;  // code words, halves a run
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-          const uint32_t x = c0[w], y = c1[w];
-          const uint32_t a0 = pair<0>(x, ktab), a1 = pair<0>(y, ktab), a2 = pair<1>(x, ktab), a3 = pair<1>(y, ktab);
-          const uint32_t b0 = pair<2>(x, ktab), b1 = pair<2>(y, ktab), b2 = pair<3>(x, ktab), b3 = pair<3>(y, ktab);
+      for (int r0 = 0; r0 < (NC == 1 ? 2 : D / 64); ++r0) {
+        uint32_t c0[HV][CW], c1[HV][CW];  // codes of tokens 16 i + g and 16 i + 8 + g
 #pragma unroll
-          for (int o = 0; o < QS; ++o) {
-            mma(sc[i], a0, a1, a2, a3, qb[o][2 * w][0], qb[o][2 * w][1]);
-            mma(sc[i], b0, b1, b2, b3, qb[o][2 * w + 1][0], qb[o][2 * w + 1][1]);
+        for (int x = 0; x < HV; ++x) {
+          const int i = NC == 1 ? r0 : x, at_word = NC == 1 ? 0 : 8 * r0;
+          lds_words(from + (16 * i + g) * (D / 2) + q4 * (D / 8) + at_word, c0[x]);
+          lds_words(from + (16 * i + 8 + g) * (D / 2) + q4 * (D / 8) + at_word, c1[x]);
+        }
+#pragma unroll
+        for (int w = 0; w < CW; ++w) {
+          uint4 qv[NC][QS];
+#pragma unroll
+          for (int ct = 0; ct < NC; ++ct)
+#pragma unroll
+            for (int o = 0; o < QS; ++o) qv[ct][o] = NC == 1 ? qb[NC == 1 ? o : 0][NC == 1 ? w : 0] : load_q(o, ct, 2 * r0 + w);
+#pragma unroll
+          for (int x = 0; x < HV; ++x) {
+            const int i = NC == 1 ? r0 : x;
+            const uint32_t u = c0[x][w], v = c1[x][w];
+            const uint32_t a0 = pair<0>(u, ktab), a1 = pair<0>(v, ktab), a2 = pair<1>(u, ktab), a3 = pair<1>(v, ktab);
+            const uint32_t b0 = pair<2>(u, ktab), b1 = pair<2>(v, ktab), b2 = pair<3>(u, ktab), b3 = pair<3>(v, ktab);
+#pragma unroll
+            for (int o = 0; o < QS; ++o)
+#pragma unroll
+              for (int ct = 0; ct < NC; ++ct) mma(sc[ct][i], a0, a1, a2, a3, qv[ct][o].x, qv[ct][o].y);
+#pragma unroll
+            for (int o = 0; o < QS; ++o)
+#pragma unroll
+              for (int ct = 0; ct < NC; ++ct) mma(sc[ct][i], b0, b1, b2, b3, qv[ct][o].z, qv[ct][o].w);
           }
         }
       }
-      float t[4][2], kn[4], vn[4];
+      float kn[4], vn[4], lv[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         kn[i] = lds_f32(from + kStep * D + 4 * (8 * i + g));
         vn[i] = lds_f32(from + kStep * D + 128 + 4 * (8 * i + g));
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          t[i][o] = sc[i >> 1][2 * (i & 1) + o];
-          if (P4) t[i][o] += __shfl_xor_sync(dev::kFull, t[i][o], 2);  // the hi and lo columns
-        }
+        lv[i] = fmaxf(log2_approx(vn[i]), -64.f);
       }
-      if (t0 + kStep > full_hi || t0 < full_lo || halves != 3)
-        soft(std::true_type{}, t0, halves, t, kn, vn);
-      else
-        soft(std::false_type{}, t0, halves, t, kn, vn);
-      // weights to operand words: fp16 pairs of two rows at a token, transposed to two tokens of a row
-      uint32_t pb[QS][4];
+      const bool edge = t0 + kStep > full_hi || t0 < full_lo || halves != 3;
+      uint32_t pb[NC][QS][4];
+      auto weights = [&](auto tile) {
+        constexpr int CT = decltype(tile)::value;
+        float t[4][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 hi = __floats2half2_rn(t[i][0], t[i][1]);
-        const float2 back = __half22float2(hi);
-        const __half2 lo = __floats2half2_rn(t[i][0] - back.x, t[i][1] - back.y);
-        const uint32_t wh = *reinterpret_cast<const uint32_t *>(&hi), wl = *reinterpret_cast<const uint32_t *>(&lo);
-        if (P4) {
-          pb[0][i] = transpose8(q4 < 2 ? wh : wl);
-        } else {
-          pb[0][i] = transpose8(wh);
-          pb[QS - 1][i] = transpose8(wl);
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            t[i][o] = sc[CT][i >> 1][2 * (i & 1) + o];
+            if (P4) t[i][o] += __shfl_xor_sync(dev::kFull, t[i][o], 2);  // the hi and lo columns
+          }
+        if (edge)
+          soft(std::true_type{}, tile, t0, halves, t, kn, vn, lv);
+        else
+          soft(std::false_type{}, tile, t0, halves, t, kn, vn, lv);
+        // weights to operand words: fp16 pairs of two rows at a token, transposed to two tokens of a row
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 hi = __floats2half2_rn(t[i][0], t[i][1]);
+          const float2 back = __half22float2(hi);
+          const __half2 lo = __floats2half2_rn(t[i][0] - back.x, t[i][1] - back.y);
+          const uint32_t wh = *reinterpret_cast<const uint32_t *>(&hi), wl = *reinterpret_cast<const uint32_t *>(&lo);
+          if (P4) {
+            pb[CT][0][i] = transpose8(q4 < 2 ? wh : wl);
+          } else {
+            pb[CT][0][i] = transpose8(wh);
+            if (HL) pb[CT][QS - 1][i] = transpose8(wl);
+          }
         }
-      }
+      };
+      weights(std::integral_constant<int, 0>{});
+      if constexpr (NC == 2) weights(std::integral_constant<int, 1>{});
       // ---- values: tokens 2 q4 and 2 q4 + 1 interleaved (even and odd coordinates apart)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -601,7 +655,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
             constexpr int K = decltype(k)::value;
             const uint32_t a0 = pair<K>(e0, vtab), a1 = pair<K>(o0, vtab), a2 = pair<K>(e1, vtab), a3 = pair<K>(o1, vtab);
 #pragma unroll
-            for (int o = 0; o < QS; ++o) mma(acc[4 * w + K], a0, a1, a2, a3, pb[o][2 * i], pb[o][2 * i + 1]);
+            for (int o = 0; o < QS; ++o)
+#pragma unroll
+              for (int ct = 0; ct < NC; ++ct)
+                mma(acc[ct][4 * w + K], a0, a1, a2, a3, pb[ct][o][2 * i], pb[ct][o][2 * i + 1]);
           };
           tile(std::integral_constant<int, 0>{});
           tile(std::integral_constant<int, 1>{});
@@ -616,28 +673,32 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
 
     // ---- the warps' sums
 #pragma unroll
-    for (int o = 0; o < 2; ++o) {
-      float t = l[o];
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) t += __shfl_xor_sync(dev::kFull, t, x);
-      if (g == 0 && 2 * q4 < RG) {
-        s_m[warp][2 * q4 + o] = M[o];
-        s_l[warp][2 * q4 + o] = t;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < MV; ++j)
+    for (int ct = 0; ct < NC; ++ct) {
+      const int i0 = 8 * ct + 2 * q4;
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
-        float x = acc[j][o], y = acc[j][2 + o];
-        if (P4) {
-          x += __shfl_xor_sync(dev::kFull, x, 2);
-          y += __shfl_xor_sync(dev::kFull, y, 2);
+        float t = l[ct][o];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) t += __shfl_xor_sync(dev::kFull, t, x);
+        if (g == 0 && i0 < RG) {
+          s_m[warp][i0 + o] = M[ct][o];
+          s_l[warp][i0 + o] = t;
         }
-        if (2 * q4 < RG)
-          *reinterpret_cast<float2 *>(parts + ((size_t)warp * kMaxRows + 2 * q4 + o) * PITCH + 16 * j + 2 * g) =
-              make_float2(x, y);
       }
+#pragma unroll
+      for (int j = 0; j < MV; ++j)
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          float x = acc[ct][j][o], y = acc[ct][j][2 + o];
+          if (P4) {
+            x += __shfl_xor_sync(dev::kFull, x, 2);
+            y += __shfl_xor_sync(dev::kFull, y, 2);
+          }
+          if (i0 < RG)
+            *reinterpret_cast<float2 *>(parts + ((size_t)warp * kMaxRows + i0 + o) * PITCH + 16 * j + 2 * g) =
+                make_float2(x, y);
+        }
+    }
     __syncthreads();
     const bool starts = s0 == req.lo, ends = s1 == req.hi;
     // each warp's factor for each row of its group
@@ -794,11 +855,11 @@ __global__ void __launch_bounds__(D * (P4 ? 4 : 8)) paged_merge_kernel(const __g
   }
 }
 
-template <int D, bool P4, bool MULTI, bool UNIT>
+template <int D, int RG, bool MULTI, bool UNIT, bool HL>
 cudaError_t run_rows(const RowsParams &p, cudaStream_t s) {
   // dynamic shared memory starts behind the 1 KiB that the system keeps
   const int dyn = (int)smem_end<D>() - 1024;
-  auto kern = paged_rows_kernel<D, P4, MULTI, UNIT>;
+  auto kern = paged_rows_kernel<D, RG, MULTI, UNIT, HL>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
   if (e != cudaSuccess) return e;
   const int ctas = decode_ctas();
@@ -807,23 +868,37 @@ cudaError_t run_rows(const RowsParams &p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at{};
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)p.groups);
-  cfg.blockDim = dim3(D * (P4 ? 4 : 8));
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(p.groups * (RG > 8 ? RG / 8 : 1)));
+  cfg.blockDim = dim3(D * (RG == 4 ? 4 : 8));
   cfg.stream = s;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, P4>, p);
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, RG == 4>, p);
 }
 
 template <int D>
-cudaError_t run_d(const RowsParams &p, bool p4, cudaStream_t s) {
+cudaError_t run_d(const RowsParams &p, int rg, cudaStream_t s) {
   const CacheView &k = p.a.k, &v = p.a.v;
   const bool unit = k.sn == 1 && v.sn == 1 && k.sb == v.sb && k.sh == v.sh;
-  if (p4) return unit ? run_rows<D, true, false, true>(p, s) : run_rows<D, true, false, false>(p, s);
-  if (p.groups == 1) return unit ? run_rows<D, false, false, true>(p, s) : run_rows<D, false, false, false>(p, s);
-  return unit ? run_rows<D, false, true, true>(p, s) : run_rows<D, false, true, false>(p, s);
+  auto run = [&](auto rg_, auto multi, auto hl) {
+    constexpr int RG = decltype(rg_)::value;
+    constexpr bool M = decltype(multi)::value, HL = decltype(hl)::value;
+    return unit ? run_rows<D, RG, M, true, HL>(p, s) : run_rows<D, RG, M, false, HL>(p, s);
+  };
+  using R4 = std::integral_constant<int, 4>;
+  using R8 = std::integral_constant<int, 8>;
+  using R16 = std::integral_constant<int, 16>;
+  const std::true_type yes{};
+  const std::false_type no{};
+  if (rg == 4) return run(R4{}, no, yes);
+  const bool hl = p.a.dtype != TQ_BF16;
+  if (rg == 8) {
+    if (p.groups == 1) return hl ? run(R8{}, no, yes) : run(R8{}, no, no);
+    return run(R8{}, yes, yes);
+  }
+  return p.groups == 1 ? run(R16{}, no, no) : run(R16{}, yes, no);
 }
 
 }  // namespace
@@ -843,9 +918,10 @@ cudaError_t launch_paged_rows(const PagedAttentionArgs &a, cudaStream_t s) {
   p.slots = p.v_unit + 4;
   // rows of a request and KV head that go through its tokens together; more of them are further units
   const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv);
-  const bool p4 = rows <= 4;
-  p.groups = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
-  return a.kq.d == 64 ? run_d<64>(p, p4, s) : run_d<128>(p, p4, s);
+  const int rg = rows <= 4 ? 4 : rows <= 8 || a.dtype != TQ_BF16 ? 8 : 16;
+  p.groups = (int)((rows + rg - 1) / rg);
+  p.groups = p.groups > kUnitRows / rg ? kUnitRows / rg : p.groups;
+  return a.kq.d == 64 ? run_d<64>(p, rg, s) : run_d<128>(p, rg, s);
 }
 
 }  // namespace tq
