@@ -98,8 +98,8 @@ struct RowsParams {
   PagedAttentionArgs a;
   int groups;       // warps are in so many groups of 4, 8 or 16 query rows, which go through the same steps
   float *slots;     // [2 * ctas][kUnitRows][D + 2]: sums, then M and L
-  int4 *desc;       // [2 * ctas]: {pieces, rows, first row, head}, {first query row} of the unit that starts last in a range
-  float *v_unit;    // what the values' table is to be divided by
+  int4 *desc;       // [2 * ctas]: {pieces, rows, first row, head}, {first query row, what the values' table is to be divided
+                    // by} of the unit that starts last in a range
   unsigned *faults;
 };
 
@@ -132,7 +132,13 @@ __device__ __forceinline__ Req load_req(const PagedAttentionArgs &a, int r, int 
   return q;
 }
 
-__device__ __forceinline__ int64_t weight(const Req &q, int Hkv) { return (int64_t)q.tiles * Hkv * (q.hi - q.lo); }
+// Places of a unit in the line: its steps, and before them `cost` for what it costs besides (the first copies' way, the
+// merge of the warps), so that ranges of many short units do not end late: 16 requests of up to 65536 tokens 148 us,
+// without it 188; 64 of up to 4001 with 16 rows 89 us, without it 155.  Flat between 30 and 50 steps of all 12 warps.
+constexpr int kUnitCost = 36;
+__device__ __forceinline__ int64_t weight(const Req &q, int Hkv, int cost) {
+  return (int64_t)q.tiles * Hkv * (q.hi - q.lo + cost);
+}
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
@@ -234,6 +240,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
   const int groups = MULTI ? p.groups : 1;
   const int RT = RG * groups, WG = W / groups;         // rows of a unit, warps of a group
   const int group = MULTI ? warp / WG : 0, wg = warp - group * WG, gr = RG * group;  // the warp's group, place in it, first row
+  const int cost = kUnitCost / groups;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const uint32_t dyn = (uint32_t)__cvta_generic_to_shared(s_raw);
   uint32_t dyn_bytes;
@@ -253,7 +260,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
   int64_t mine = 0;  // steps, and units from bit 42 on
   for (int r = tid * per; r < min((tid + 1) * per, a.R); ++r) {
     const Req q = load_req(a, r, RT, p.faults);
-    mine += weight(q, a.Hkv) + (int64_t)((uint64_t)q.tiles * (uint64_t)a.Hkv << 42);
+    mine += weight(q, a.Hkv, cost) + (int64_t)((uint64_t)q.tiles * (uint64_t)a.Hkv << 42);
   }
   __syncthreads();
   find_scales(a.kq.centroids, a.vq.centroids, tid, NT, sm.key);
@@ -308,7 +315,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
     r_base = s_base[i];
     for (; r < a.R; ++r) {
       req = load_req(a, r, RT, p.faults);
-      const int64_t w = weight(req, a.Hkv);
+      const int64_t w = weight(req, a.Hkv, cost);
       if (at < r_base + w) break;
       r_base += w;
     }
@@ -331,11 +338,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
 
   for (bool tables = false; at < end && r < a.R; tables = true) {
     // ---- the piece: steps [s0, s1) of unit (r, h, tile)
-    const int len = req.hi - req.lo;
+    const int len = req.hi - req.lo + cost;
     const int64_t x = at - r_base;
     const int unit = x < INT_MAX ? (int)((uint32_t)x / (uint32_t)len) : (int)(x / len);
-    const int s0 = req.lo + (int)(x - (int64_t)unit * len);
-    const int s1 = (int)min((int64_t)req.hi, s0 + (end - at));
+    const int x0 = (int)(x - (int64_t)unit * len), x1 = (int)min((int64_t)len, x0 + (end - at));
+    if (x1 <= cost) break;  // the range ends before the unit's first step
+    const int s0 = req.lo + max(x0 - cost, 0), s1 = req.lo + x1 - cost;
     const int h = unit / req.tiles, tile = unit - h * req.tiles;
     const int row0 = tile * RT;
     const int nrows = min(RT, req.n * G - row0);
@@ -398,10 +406,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
         float unit;
         const float s = scale_of(sm.key[warp], NT, cent, unit);
         if (lane < 16) sm.level[warp][lane] = __float2half_rn(s * __ldg(cent + lane));
-        if (lane == 0) {
-          s_scale[warp] = unit;
-          if (warp == 1 && c == 0) *p.v_unit = unit;  // for the merge
-        }
+        if (lane == 0) s_scale[warp] = unit;
       }
       __syncthreads();
       uint4 *tab = reinterpret_cast<uint4 *>(s_raw + (kTabAddr - dyn));
@@ -562,13 +567,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[ct][i][e] = 0.f;
       // a query operand that is not kept is read once for both halves, so their codes come in runs of two words
-      constexpr int CW = NC == 1 ? D / 32 : 2, HV = NC == 1 ? 1 : 2;  // code words, halves a run
+      constexpr int CW = 2, HV = 2;  // code words, halves a run
 #pragma unroll
-      for (int r0 = 0; r0 < (NC == 1 ? 2 : D / 64); ++r0) {
+      for (int r0 = 0; r0 < D / 32 / CW; ++r0) {
         uint32_t c0[HV][CW], c1[HV][CW];  // codes of tokens 16 i + g and 16 i + 8 + g
 #pragma unroll
         for (int x = 0; x < HV; ++x) {
-          const int i = NC == 1 ? r0 : x, at_word = NC == 1 ? 0 : 8 * r0;
+          const int i = x, at_word = 4 * CW * r0;
           lds_words(from + (16 * i + g) * (D / 2) + q4 * (D / 8) + at_word, c0[x]);
           lds_words(from + (16 * i + 8 + g) * (D / 2) + q4 * (D / 8) + at_word, c1[x]);
         }
@@ -578,10 +583,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
 #pragma unroll
           for (int ct = 0; ct < NC; ++ct)
 #pragma unroll
-            for (int o = 0; o < QS; ++o) qv[ct][o] = NC == 1 ? qb[NC == 1 ? o : 0][NC == 1 ? w : 0] : load_q(o, ct, 2 * r0 + w);
+            for (int o = 0; o < QS; ++o) qv[ct][o] = NC == 1 ? qb[NC == 1 ? o : 0][NC == 1 ? CW * r0 + w : 0] : load_q(o, ct, CW * r0 + w);
 #pragma unroll
           for (int x = 0; x < HV; ++x) {
-            const int i = NC == 1 ? r0 : x;
+            const int i = x;
             const uint32_t u = c0[x][w], v = c1[x][w];
             const uint32_t a0 = pair<0>(u, ktab), a1 = pair<0>(v, ktab), a2 = pair<1>(u, ktab), a3 = pair<1>(v, ktab);
             const uint32_t b0 = pair<2>(u, ktab), b1 = pair<2>(v, ktab), b2 = pair<3>(u, ktab), b3 = pair<3>(v, ktab);
@@ -744,7 +749,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
     }
     if (starts && !ends) {
       // CTAs whose ranges the unit reaches: the last holds its last step
-      const int64_t last = at + len - 1;
+      const int64_t last = at + (len - x0) - 1;
       int e = c;
       if (last >= end) {
         e = (int)(last * ctas / total);  // a first guess
@@ -752,15 +757,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
         while (e > c && cut(e) > last) --e;
       }
       desc = make_int4(e - c + 1, nrows, row0, h);
-      where = make_int4(req.q0, 0, 0, 0);
+      where = make_int4(req.q0, __float_as_int(s_scale[1]), 0, 0);
     }
     __syncthreads();
-    at += s1 - s0;
-    if (at < end && at - r_base == weight(req, a.Hkv)) {
+    at += x1 - x0;
+    if (at < end && at - r_base == weight(req, a.Hkv, cost)) {
       r_base = at;
       while (++r < a.R) {
         req = load_req(a, r, RT, p.faults);
-        if (weight(req, a.Hkv) > 0) break;
+        if (weight(req, a.Hkv, cost) > 0) break;
       }
     }
   }
@@ -785,7 +790,7 @@ __global__ void __launch_bounds__(D * (P4 ? 4 : 8)) paged_merge_kernel(const __g
   const int r8 = RT * blockIdx.y;  // the block's first row of the unit
   const int n = desc.x, nrows = min(RT, desc.y - r8), row0 = desc.z + r8;
   if (n == 0 || nrows <= 0) return;
-  const float vs = __ldcg(p.v_unit);
+  const float vs = __int_as_float(where.y);
   const int G = a.Hq / a.Hkv;
   // piece k's slot
   auto slot = [&](int k) { return p.slots + (size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * kUnitRows * (D + 2) + r8 * (D + 2); };
@@ -905,7 +910,7 @@ cudaError_t run_d(const RowsParams &p, int rg, cudaStream_t s) {
 
 size_t paged_rows_workspace(int d) {
   const size_t ctas = decode_ctas();
-  return 2 * ctas * sizeof(int4) + 16 + 2 * ctas * kUnitRows * (d + 2) * sizeof(float);
+  return 2 * ctas * sizeof(int4) + 2 * ctas * kUnitRows * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_rows(const PagedAttentionArgs &a, cudaStream_t s) {
@@ -914,8 +919,7 @@ cudaError_t launch_paged_rows(const PagedAttentionArgs &a, cudaStream_t s) {
   const cudaError_t e = fault_word(&p.faults);
   if (e != cudaSuccess) return e;
   p.desc = static_cast<int4 *>(a.ws);
-  p.v_unit = reinterpret_cast<float *>(p.desc + 2 * decode_ctas());
-  p.slots = p.v_unit + 4;
+  p.slots = reinterpret_cast<float *>(p.desc + 2 * decode_ctas());
   // rows of a request and KV head that go through its tokens together; more of them are further units
   const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv);
   const int rg = rows <= 4 ? 4 : rows <= 8 || a.dtype != TQ_BF16 ? 8 : 16;
