@@ -2,7 +2,8 @@
 // prefill, and decode with more rows a KV head than the small tiles take.
 //
 // A unit is (request, KV head, tile of query rows), a block 128 cached tokens.
-// All units' blocks form one line cut evenly over one persistent CTA an SM;
+// All units' blocks, and a fixed cost of each unit, form one line cut evenly
+// over one persistent CTA an SM;
 // units cut by a range's end leave partial sums that a last kernel merges in
 // the order of the tokens.
 //
@@ -31,7 +32,7 @@
 // to its values' product, two sets deep: a softmax takes 2.4 to 3.5 thousand
 // cycles, the products about 2 thousand.  Measured on a B200, bf16, 32 / 8
 // heads, d = 128: 3 requests of 2048 rows on up to 16384 tokens, causal (920
-// GFLOP), 1499 us, 614 TFLOP/s; 2048 rows on 8192 tokens 419 us.
+// GFLOP), 1376 us, 669 TFLOP/s; 2048 rows on 8192 tokens 414 us.
 
 #include "../../include/tq.h"
 #include "tq_device.cuh"
@@ -48,6 +49,10 @@ namespace {
 using namespace paged;
 
 constexpr int kBlk = 128;                 // tokens per block
+// What a unit costs in the line besides its blocks, in blocks (its rows' way to the operand tiles, the first block's way
+// through the pipeline, the outputs), so that ranges of many short units do not end late: 8 requests of 512 rows and up to
+// 4001 tokens 232 us, without it 547; 3 of 2048 rows and up to 16384 tokens 1376, without it 1496.  9 is slower again.
+constexpr int kUnitCost = 5;
 constexpr int kThreads = 512;             // 2 x 4 softmax warps, 4 warps decode K and 4 V
 constexpr uint32_t kTabAddr = 0x10000u;   // the pair tables: 64 KiB at this shared address
 constexpr uint32_t kHighAddr = 0x20000u;  // V, K and the second query tile
@@ -67,7 +72,7 @@ struct TileParams {
   const float *qf;         // [T * Hq] the factor their scores still need (softmax scale, log2 e, row scale)
   int64_t max_tiles;       // that `line` has room for
   int32_t *first;          // [R + 1] first tile of each request
-  int64_t *line;           // [tiles + 1] blocks (of one KV head) before each tile
+  int64_t *line;           // [tiles + 1] places (of one KV head) before each tile: kUnitCost and its blocks
   float *slots;            // [2 * ctas][rt][D + 4]: a row's sums, then M and L
   int4 *desc;              // [ctas]
   float *v_unit;           // what the values' table is to be divided by
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(256) paged_tile_prep_kernel(const __grid_const
         }
         int b0, b1, first;
         tile_blocks(a, load_req(a, i, p.faults), p.rt, (int)t - p.first[i], b0, b1, first);
-        mine = b1 - b0;
+        mine = b1 - b0 + kUnitCost;
       }
       const int64_t before = blocks + scan<256>(mine, s_warp, &all);
       if (t < tiles) p.line[t] = before;
@@ -237,6 +242,7 @@ __global__ void __launch_bounds__(256) paged_tile_prep_kernel(const __grid_const
 struct Piece {
   int r, h, row0, nrows, q0, n, kv, first;
   int b0, b1;        // blocks
+  int places;        // of the line
   int starts, ends;  // whether they hold the unit's first and last block
 };
 
@@ -426,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
       items_done[1] += !both ? 0 : SPLIT ? nblk / 2 : nblk;
       ++pieces_done[0];
       pieces_done[1] += both;
-      at += nblk;
+      at += q.places;
       umma::fence_before();
       __syncthreads();
       umma::fence_after();
@@ -434,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
     if (at >= end) return false;
     // ---- the piece: one thread finds the first and walks on from unit to unit
     if (tid == 0) {
-      int skip = 0;  // blocks of the unit in front of the range
+      int skip = 0;  // places of the unit in front of the range
       if (r < 0) {
         int i = 0, j = a.R;  // the last request whose line starts at or before `at`
         while (j - i > 1) {
@@ -478,13 +484,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
       q.kv = req.kv;
       q.row0 = (tile - ta) * RT;
       q.nrows = min(RT, req.n * G - q.row0);
-      q.b0 = b0 + skip;
-      q.b1 = (int)min((int64_t)b1, q.b0 + (end - at));
-      q.starts = skip == 0;
-      q.ends = q.b1 == b1;
+      const int len = b1 - b0 + kUnitCost, to = (int)min((int64_t)len, skip + (end - at));
+      q.places = to - skip;
+      q.b0 = b0 + max(skip - kUnitCost, 0);
+      q.b1 = max(b0 + to - kUnitCost, q.b0);  // none where the range ends before the unit's first block
+      q.starts = skip <= kUnitCost;
+      q.ends = to == len;
       sm.piece = q;
-      if (q.starts && !q.ends) {
-        const int64_t last = at + (b1 - b0) - 1;
+      if (q.starts && !q.ends && q.b1 > q.b0) {
+        const int64_t last = at + (len - skip) - 1;
         int64_t e = last * ctas / total;
         while (e < ctas - 1 && total * (e + 1) / ctas <= last) ++e;
         while (e > c && total * e / ctas > last) --e;
@@ -494,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
     __syncthreads();
     q = sm.piece;
     nblk = q.b1 - q.b0;
+    if (nblk == 0) return false;
     both = SPLIT ? nblk > 1 : q.nrows > 128;
     // ---- query rows into the operand tiles: 16-byte words of 8 coordinates
     constexpr int QB = RT * (D / 8) / kThreads;  // a thread's words, their loads in flight together
