@@ -92,7 +92,13 @@ template <int D>
 __device__ __forceinline__ void load_row(const void *p, int dt, int64_t at, int lane, float (&v)[D / 32]) {
   const uint32_t *s = reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + at + lane * (D / 32));
   uint32_t w[D / 64];
-  if constexpr (D / 64 == 2) {
+  if constexpr (D / 64 == 4) {
+    const uint4 t = __ldg(reinterpret_cast<const uint4 *>(s));
+    w[0] = t.x;
+    w[1] = t.y;
+    w[2] = t.z;
+    w[3] = t.w;
+  } else if constexpr (D / 64 == 2) {
     const uint2 t = __ldg(reinterpret_cast<const uint2 *>(s));
     w[0] = t.x;
     w[1] = t.y;
@@ -145,7 +151,9 @@ __device__ __forceinline__ void store_out(const PagedAttentionArgs &a, int64_t t
     }
   }
   uint16_t *o = static_cast<uint16_t *>(a.out) + (t * a.Hq + hq) * D + lane * (D / 32);
-  if constexpr (D / 64 == 2)
+  if constexpr (D / 64 == 4)
+    *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+  else if constexpr (D / 64 == 2)
     *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
   else
     *reinterpret_cast<uint32_t *>(o) = w[0];

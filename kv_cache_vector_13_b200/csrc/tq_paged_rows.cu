@@ -56,14 +56,15 @@ using namespace paged;
 constexpr int kStep = 32;                // tokens per step, in two halves of 16 that may lie in two pages
 constexpr uint32_t kTabAddr = 0x10000u;  // the pair tables: 64 KiB at this shared address
 constexpr uint32_t kPartAddr = 0x20000u; // the warps' partial sums
-constexpr int kMaxRows = 16;              // query rows of a group of warps
-constexpr int kUnitRows = 32;             // of a unit: up to 2 groups
 constexpr int64_t kSteps = ((int64_t)1 << 42) - 1;
 constexpr int kStages = 2;               // a warp's steps in shared memory: one worked on, one on its way
 
 template <int D>
 struct Cfg {
-  static constexpr int kWarps = 12;  // 168 registers a thread; 16 warps of 128 took 207 us where 12 take 198
+  // 168 registers a thread; 16 warps of 128 took 207 us where 12 take 198 (d = 128)
+  static constexpr int kWarps = D == 256 ? 8 : 12;
+  static constexpr int kMaxRows = D == 256 ? 8 : 16;    // query rows of a group of warps
+  static constexpr int kUnitRows = D == 256 ? 16 : 32;  // of a unit
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kPitch = D + 4;  // floats of a partial row (no bank clash between rows)
   // a step: K codes, V codes, norms of each
@@ -78,19 +79,20 @@ template <int D>
 struct Low {
   int64_t base[Cfg<D>::kThreads];  // the line at each thread's first request
   int64_t warp[Cfg<D>::kWarps];
-  alignas(16) __half q[2][kUnitRows][D + 32];  // operand columns: hi of each row, lo of each row (q_place)
-  float f[kUnitRows];                          // logit factor of each row
-  int see_lo[kUnitRows], see_hi[kUnitRows];    // the tokens that each row sees
-  float m[Cfg<D>::kWarps][kMaxRows], l[Cfg<D>::kWarps][kMaxRows];
+  alignas(16) __half q[2][Cfg<D>::kUnitRows][D + 32];  // operand columns: hi of each row, lo of each row (q_place)
+  float f[Cfg<D>::kUnitRows];                          // logit factor of each row
+  int see_lo[Cfg<D>::kUnitRows], see_hi[Cfg<D>::kUnitRows];    // the tokens that each row sees
+  float m[Cfg<D>::kWarps][Cfg<D>::kMaxRows], l[Cfg<D>::kWarps][Cfg<D>::kMaxRows];
   float scale[2];                  // what the tables' values are to be divided by
   unsigned key[2];
   __half level[2][16];             // the scaled levels
-  float e[Cfg<D>::kWarps][kMaxRows], top[kUnitRows], sum[kUnitRows];  // merge of the warps
+  float e[Cfg<D>::kWarps][Cfg<D>::kMaxRows], top[Cfg<D>::kUnitRows], sum[Cfg<D>::kUnitRows];  // merge of the warps
 };
 
 template <int D>
 __host__ __device__ constexpr uint32_t smem_end() {
-  constexpr uint32_t parts = Cfg<D>::kWarps * kMaxRows * Cfg<D>::kPitch * 4, rings = Cfg<D>::kHigh * Cfg<D>::kRing;
+  constexpr uint32_t parts = Cfg<D>::kWarps * Cfg<D>::kMaxRows * Cfg<D>::kPitch * 4, rings = Cfg<D>::kHigh * Cfg<D>::kRing;
+  static_assert(kPartAddr + (parts > rings ? parts : rings) <= 227 * 1024, "");
   return kPartAddr + (parts > rings ? parts : rings);
 }
 
@@ -196,13 +198,21 @@ __device__ __forceinline__ float lds_f32(uint32_t a) {
   return v;
 }
 
-// Where the staged V codes of token t, 16-byte word c, lie: two tokens swap
-// places in every other group of four, and word pairs in every other pair of
-// tokens, so that a half-warp's reads (8 bytes of tokens 0, 2, 4, 6) fall into
-// different banks.
+// Where the staged V codes of token t, 16-byte word c, lie, so that a
+// half-warp's reads (8 bytes of tokens 0, 2, 4, 6; a quarter-warp's 16 for d =
+// 256) fall into different banks: two tokens swap places in every other group
+// of four, and word pairs in every other pair of tokens; for d = 256, word
+// pairs are exchanged by the pair of tokens.
 template <int D>
 __device__ __forceinline__ uint32_t v_place(int t, int c) {
+  if constexpr (D == 256) return (uint32_t)(t * (D / 2) + (c ^ (((t >> 1) & 3) << 1)) * 16);
   return (uint32_t)((t ^ ((t >> 2) & 1)) * (D / 2) + (D == 128 ? (c ^ (((t >> 1) & 1) << 1)) * 16 : c * 16));
+}
+// And those of K: for d = 256, whose records are as long as all banks, words
+// are exchanged by the token.
+template <int D>
+__device__ __forceinline__ uint32_t k_place(int t, int c) {
+  return (uint32_t)(t * (D / 2) + (D == 256 ? c ^ (t & 7) : c) * 16);
 }
 
 // Where coordinate k of a query row lies: a lane's words of two k steps are 16
@@ -219,6 +229,7 @@ __device__ __forceinline__ int q_place(int k) {
 template <int D, int RG, bool MULTI, bool UNIT, bool HL>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr int W = Cfg<D>::kWarps, NT = Cfg<D>::kThreads, PITCH = Cfg<D>::kPitch;
+  constexpr int kMaxRows = Cfg<D>::kMaxRows, kUnitRows = Cfg<D>::kUnitRows;
   constexpr bool P4 = RG == 4;
   constexpr int NC = RG == 16 ? 2 : 1;  // column tiles
   constexpr int KS = D / 16;      // k steps of the scores
@@ -329,6 +340,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
   const uint8_t *kc_lane = a.k.codes + (lane / (D / 32)) * k_tok + (lane % (D / 32)) * 16;
   const uint8_t *vc_lane = a.v.codes + (lane / (D / 32)) * v_tok + (lane % (D / 32)) * 16;
   const float *n_lane = lane < 16 ? a.k.norms + lane * a.k.sn : a.v.norms + (lane - 16) * a.v.sn;
+  const uint32_t k_to = k_place<D>(lane / (D / 32), lane % (D / 32));
   const uint32_t v_to = v_place<D>(lane / (D / 32), lane % (D / 32)), n_to = 4 * (lane & 15) + (lane < 16 ? 0 : 128);
   // and the lane's reads: V of tokens 2 q4 and 2 q4 + 1
   const uint32_t v_at0 = v_place<D>(2 * q4, g * (D / 16) / 16) + (g * (D / 16)) % 16;
@@ -384,8 +396,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
           const uint8_t *ks = kc_lane + kr * (D / 2), *vs = vc_lane + vr * (D / 2);
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) {
-            cp_async16(to + 16 * lane + hf * (8 * D) + 512 * i, ks + (UNIT ? 512 * i : 8 * i * k_tok));
-            cp_async16(to + kStep * (D / 2) + v_to + hf * (8 * D) + 512 * i, vs + (UNIT ? 512 * i : 8 * i * v_tok));
+            constexpr int TI = 1024 / D;                    // tokens of 32 lanes
+            const uint32_t turn = D == 256 ? 64 * (i & 1) : 0;  // of k_place and v_place, TI i tokens on
+            cp_async16(to + (k_to ^ turn) + hf * (8 * D) + 512 * i, ks + (UNIT ? 512 * i : TI * i * k_tok));
+            cp_async16(to + kStep * (D / 2) + (v_to ^ turn) + hf * (8 * D) + 512 * i, vs + (UNIT ? 512 * i : TI * i * v_tok));
           }
           // lanes 0..15 the norms of K, the others those of V
           cp_async4(to + kStep * D + n_to + 64 * hf, n_lane + (UNIT || lane < 16 ? kr : vr));
@@ -574,8 +588,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
 #pragma unroll
         for (int x = 0; x < HV; ++x) {
           const int i = x, at_word = 4 * CW * r0;
-          lds_words(from + (16 * i + g) * (D / 2) + q4 * (D / 8) + at_word, c0[x]);
-          lds_words(from + (16 * i + 8 + g) * (D / 2) + q4 * (D / 8) + at_word, c1[x]);
+          const uint32_t k_at = k_place<D>(g, (q4 * (D / 8) + at_word) / 16) + (q4 * (D / 8) + at_word) % 16;
+          lds_words(from + 16 * i * (D / 2) + k_at, c0[x]);
+          lds_words(from + (16 * i + 8) * (D / 2) + k_at, c1[x]);
         }
 #pragma unroll
         for (int w = 0; w < CW; ++w) {
@@ -778,9 +793,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
 // Merges the pieces of the unit that starts last in CTA c's range and goes on
 // behind it, in the order of the tokens: a block a unit and group of rows, a
 // coordinate of a row a thread.
-template <int D, bool P4>
-__global__ void __launch_bounds__(D * (P4 ? 4 : 8)) paged_merge_kernel(const __grid_constant__ RowsParams p) {
-  constexpr int RT = P4 ? 4 : 8;
+template <int D, int RT>
+__global__ void __launch_bounds__(D * RT) paged_merge_kernel(const __grid_constant__ RowsParams p) {
   __shared__ float s_y[RT][D], s_top[RT];
   __shared__ float s_e[RT][32], s_l[RT];
   const PagedAttentionArgs &a = p.a;
@@ -793,7 +807,7 @@ __global__ void __launch_bounds__(D * (P4 ? 4 : 8)) paged_merge_kernel(const __g
   const float vs = __int_as_float(where.y);
   const int G = a.Hq / a.Hkv;
   // piece k's slot
-  auto slot = [&](int k) { return p.slots + (size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * kUnitRows * (D + 2) + r8 * (D + 2); };
+  auto slot = [&](int k) { return p.slots + (size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * Cfg<D>::kUnitRows * (D + 2) + r8 * (D + 2); };
   const int i = tid / D, k = tid % D;
   // the first pieces' sums are on their way while their factors are made
   constexpr int N = 20;
@@ -873,14 +887,15 @@ cudaError_t run_rows(const RowsParams &p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at{};
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(p.groups * (RG > 8 ? RG / 8 : 1)));
-  cfg.blockDim = dim3(D * (RG == 4 ? 4 : 8));
+  constexpr int RT = D == 256 || RG == 4 ? 4 : 8;  // rows of a block
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(p.groups * RG / RT));
+  cfg.blockDim = dim3(D * RT);
   cfg.stream = s;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, RG == 4>, p);
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, RT>, p);
 }
 
 template <int D>
@@ -899,18 +914,21 @@ cudaError_t run_d(const RowsParams &p, int rg, cudaStream_t s) {
   const std::false_type no{};
   if (rg == 4) return run(R4{}, no, yes);
   const bool hl = p.a.dtype != TQ_BF16;
-  if (rg == 8) {
+  if constexpr (D == 256) {
     if (p.groups == 1) return hl ? run(R8{}, no, yes) : run(R8{}, no, no);
-    return run(R8{}, yes, yes);
+    return hl ? run(R8{}, yes, yes) : run(R8{}, yes, no);
+  } else {
+    if (rg == 8 && p.groups == 1) return hl ? run(R8{}, no, yes) : run(R8{}, no, no);
+    if (rg == 8) return run(R8{}, yes, yes);
+    return p.groups == 1 ? run(R16{}, no, no) : run(R16{}, yes, no);
   }
-  return p.groups == 1 ? run(R16{}, no, no) : run(R16{}, yes, no);
 }
 
 }  // namespace
 
 size_t paged_rows_workspace(int d) {
   const size_t ctas = decode_ctas();
-  return 2 * ctas * sizeof(int4) + 2 * ctas * kUnitRows * (d + 2) * sizeof(float);
+  return 2 * ctas * sizeof(int4) + 2 * ctas * (d == 256 ? Cfg<256>::kUnitRows : Cfg<128>::kUnitRows) * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_rows(const PagedAttentionArgs &a, cudaStream_t s) {
@@ -922,10 +940,10 @@ cudaError_t launch_paged_rows(const PagedAttentionArgs &a, cudaStream_t s) {
   p.slots = reinterpret_cast<float *>(p.desc + 2 * decode_ctas());
   // rows of a request and KV head that go through its tokens together; more of them are further units
   const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv);
-  const int rg = rows <= 4 ? 4 : rows <= 8 || a.dtype != TQ_BF16 ? 8 : 16;
-  p.groups = (int)((rows + rg - 1) / rg);
-  p.groups = p.groups > kUnitRows / rg ? kUnitRows / rg : p.groups;
-  return a.kq.d == 64 ? run_d<64>(p, rg, s) : run_d<128>(p, rg, s);
+  const int rg = rows <= 4 ? 4 : rows <= 8 || a.dtype != TQ_BF16 || a.kq.d == 256 ? 8 : 16;
+  const int unit_rows = a.kq.d == 256 ? Cfg<256>::kUnitRows : Cfg<128>::kUnitRows;
+  p.groups = (int)((rows < unit_rows ? rows + rg - 1 : unit_rows) / rg);
+  return a.kq.d == 64 ? run_d<64>(p, rg, s) : a.kq.d == 128 ? run_d<128>(p, rg, s) : run_d<256>(p, rg, s);
 }
 
 }  // namespace tq
