@@ -517,6 +517,46 @@ def test_pages_in_another_layout():
     check_attention((kq, vq, q, kc, t(vc), table, kv_lens, cu))
 
 
+def other_layout(c, order):
+    """The cache with pages, heads and tokens in another order in memory."""
+    back = [order.index(i) for i in range(3)]
+    return api.PackedCache(c.codes.permute(*order, 3).contiguous().permute(*back, 3),
+                           c.norms.permute(*order).contiguous().permute(*back))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("G,qs", [(1, [3, 1, 1]), (2, [4, 0, 1]), (4, [4, 1, 3]), (8, [4, 1, 2])])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_rows_of_a_unit_in_another_layout(d, G, qs, dtype):
+    """3 to 32 rows a request and head, caches whose tokens do not lie side by side, K and V laid out apart."""
+    p = list(paged_problem(d + G, qs, [600, 47, 1], 2 * G, 2, d, 48, dtype))
+    poison_unseen(p[3], p[4], p[5], p[6])
+    p[3] = other_layout(p[3], (0, 2, 1))
+    check_attention(p)
+    p[4] = other_layout(p[4], (2, 1, 0))
+    check_attention(p, window=40)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("G,qs,kv", [(4, [5, 1, 9], [300, 33, 9]), (8, [3, 40, 1], [129, 40, 2000]), (1, [130, 16], [700, 16])])
+@pytest.mark.parametrize("window", [0, 29])
+def test_ragged_rows_of_256(G, qs, kv, window, dtype):
+    p = paged_problem(G, qs, kv, G * 2, 2, 256, 16, dtype)
+    poison_unseen(p[3], p[4], p[5], p[6])
+    check_attention(p, window=window)
+    if not window:
+        check_attention(p, causal=False)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("qs,kv", [([1], [1]), ([1], [40]), ([70], [70]), ([1] * 300, [(17 * i) % 90 for i in range(300)]),
+                                   ([40] + [1] * 20, [40] + [3000] + [5] * 19)])
+def test_short_units_beside_long_ones(d, qs, kv):
+    """Units of a step or none beside long ones, and fewer steps than there are SMs."""
+    check_attention(paged_problem(len(qs) + d, qs, kv, 1, 1, d, 16, torch.bfloat16))
+
+
+
 def test_a_nan_in_a_seen_record_reaches_its_rows_only():
     kq, vq, q, kc, vc, table, kv_lens, cu = paged_problem(14, [1, 3], [40, 70], 4, 2, 128, 16, torch.bfloat16)
     vc.norms[table[0, 1].long(), 1, 3] = float("nan")
