@@ -18,12 +18,13 @@ size_t paged_attention_workspace(int R, int64_t T, int Hq, int Hkv, int d) {
 }
 
 cudaError_t launch_paged_attention(const PagedAttentionArgs &a, cudaStream_t s) {
-  // Query rows of a request and KV head.  The small tiles decode the cache once for 8 or 16 rows, the large ones for 128
-  // or 256, with more work around each block: 64 requests of up to 4001 tokens, 64 / 8 heads, us, small and large tiles:
-  // 16 rows 89 and 204 (bf16), 120 and 283 (fp16); 32 rows 150 and 207, 201 and 285; 64 rows 244 and 213, 335 and 294.
+  // Query rows of a request and KV head.  The small tiles decode the cache once for 16 rows, the large ones for 128 or
+  // 256, with more work around each block: 64 requests of up to 4001 tokens, 64 / 8 heads, us, small and large tiles:
+  // bf16 16 rows 89 and 204, 32 rows 149 and 207, 40 rows 194 and 210, 48 rows 216 and 211; fp16 (large tiles of 128
+  // rows, and twice the products) 32 rows 181 and 284, 48 rows 261 and 289, 64 rows 293 and 292.
   // The large tiles' operands and tables have no room for d = 256.
   const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv);
-  return rows <= 32 || a.kq.d == 256 ? launch_paged_rows(a, s) : launch_paged_tile(a, s);
+  return rows <= (a.dtype == TQ_BF16 ? 40 : 48) || a.kq.d == 256 ? launch_paged_rows(a, s) : launch_paged_tile(a, s);
 }
 
 }  // namespace tq

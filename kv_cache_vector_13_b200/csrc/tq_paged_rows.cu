@@ -1,43 +1,51 @@
 // Attention of a few query rows a request over a paged 4-bit cache (sm_100a):
-// decode, and the verification of a few draft tokens.
+// decode, and the verification of a few draft tokens; for d = 256 any number
+// of rows.
 //
 // Work: a unit is (request, KV head, tile of query rows), a step 32 cached
-// tokens.  All units' steps form one line, cut into equal ranges, one a CTA
-// (one persistent CTA an SM), so requests of any lengths balance; a CTA's
-// part of a unit is a piece, whose steps its warps take in turn.  Units cut by
-// a range's end leave partial sums that a second kernel merges, in the order
-// of the tokens, so the result does not depend on timing.
+// tokens.  All units' steps, and a fixed cost of each unit, form one line, cut
+// into equal ranges, one a CTA (one persistent CTA an SM), so requests of any
+// lengths balance; a CTA's part of a unit is a piece, whose steps its warps
+// take in turn.  Units cut by a range's end leave partial sums that a second
+// kernel merges, in the order of the tokens, so the result does not depend on
+// timing.
 //
 // A step of a warp: S^T = K Q^T and O^T += V^T P^T with mma.m16n8k16 (fp16,
 // fp32 sums), the tokens (then the coordinates) being the 16 rows and the
 // query rows the 8 columns, and the running softmax in between.  Query rows
-// and weights are carried as fp16 pairs hi + lo: up to 4 rows a tile put both
-// into one product, as columns g and g + 4 (S and O are the sums of the two);
-// up to 8 take two products into the same sums.  Codes become operand words
-// without arithmetic: a code byte (two codes) indexes a 256-entry table of
-// fp16 centroid pairs, one copy per lane, placed so that one byte permute
-// forms the shared address.  For K the pair is two coordinates of a token; for
-// V the codes of two tokens are first interleaved, so the pair is two tokens
-// at one coordinate.  The order of coordinates within the products is free, so
-// every lane loads whole 16-byte (K) and 8-byte (V) runs of a record.  Norms
-// enter behind the products: ||k|| scales the logit, ||v|| the weight.
+// and weights are fp16 pairs hi + lo: up to 4 rows a tile put both into one
+// product, as columns g and g + 4 (S and O are the sums of the two); more take
+// two products into the same sums.  For bf16 outputs more than 4 rows are
+// rounded once, 2^-11 against the output's 2^-8 (8 rows on 4 requests of up to
+// 65536 tokens: 61 us, with pairs 68).  Codes become operand words without
+// arithmetic: a code byte (two codes) indexes a 256-entry table of fp16
+// centroid pairs, one copy per lane, placed so that one byte permute forms the
+// shared address.  For K the pair is two coordinates of a token; for V the
+// codes of two tokens are first interleaved, so the pair is two tokens at one
+// coordinate.  The order of coordinates within the products is free, so every
+// lane loads whole runs of a record.  Norms enter behind the products: ||k||
+// scales the logit, ||v|| the weight.
 //
-// Up to 8 rows a group: a unit of more has groups of warps, each with 8 of the
-// rows, which go through the same steps together, so a record comes from
-// memory once (128 requests of 4 rows, 64 / 8 heads: 502 us as units of 8
-// rows, 404 us with groups).
+// Beyond 8 rows a warp takes 16, two column tiles, and reads the tables once
+// for both; beyond 16 two groups of warps, each with 16 of a unit's rows, go
+// through the same steps together, so a record comes from memory once.  64
+// requests of up to 4001 tokens, 16 and 32 rows, us, and with groups of 8 rows
+// instead: bf16 91 and 149 (113 and 187), fp16 109 and 181 (121 and 203).  For
+// d = 256 the registers hold one column tile, so a group is of 8 rows.
 //
 // A step's records come through a ring of two stages in shared memory a warp
 // (cp.async): the next step's are on their way while one is worked on (4
 // requests of up to 262144 tokens 206 us, against 265 with a single and 296
 // with a double buffer in registers).
 //
-// Bound by the instruction stream, 332 warp instructions per 16 tokens of a KV
-// head (128 of them the byte permutes and table reads) at 53% of the issue
-// slots.  Measured on a B200, d = 128: 16 requests of up to 65536 tokens
-// (551 MB), 32 / 8 heads, bf16, 195 us, 2.8 TB/s; 1 x 32768 tokens 23.5 us, of
-// which 11.5 are left with a single step; 128 requests of 4 rows and up to 4001
-// tokens, 64 / 8 heads, fp16, 404 us.
+// Bound by the instruction stream, about 330 warp instructions per 16 tokens
+// of a KV head (128 of them the byte permutes and table reads) at half of the
+// issue slots, and by what a piece costs besides its steps, about 5 us.
+// Measured on a B200: d = 128, 32 / 8 heads, bf16, 4 requests of up to 262144
+// tokens (731 MB) 188 us, 3.9 TB/s; 16 of up to 65536 (551 MB) 147 us, 3.7
+// TB/s; 1 x 32768 tokens 23 us, of which 11.5 are left with a single step; 128
+// requests of 4 rows and up to 4001 tokens, 64 / 8 heads, fp16, 327 us; d =
+// 256, 16 requests of up to 4001 tokens, 32 / 8 heads, bf16, 40 us.
 
 #include "../../include/tq.h"
 #include "tq_device.cuh"
@@ -913,14 +921,13 @@ cudaError_t run_d(const RowsParams &p, int rg, cudaStream_t s) {
   const std::true_type yes{};
   const std::false_type no{};
   if (rg == 4) return run(R4{}, no, yes);
-  const bool hl = p.a.dtype != TQ_BF16;
+  const bool hl = p.a.dtype != TQ_BF16, one = p.groups == 1;
+  if (rg == 8 && one) return hl ? run(R8{}, no, yes) : run(R8{}, no, no);
   if constexpr (D == 256) {
-    if (p.groups == 1) return hl ? run(R8{}, no, yes) : run(R8{}, no, no);
     return hl ? run(R8{}, yes, yes) : run(R8{}, yes, no);
   } else {
-    if (rg == 8 && p.groups == 1) return hl ? run(R8{}, no, yes) : run(R8{}, no, no);
-    if (rg == 8) return run(R8{}, yes, yes);
-    return p.groups == 1 ? run(R16{}, no, no) : run(R16{}, yes, no);
+    if (one) return hl ? run(R16{}, no, yes) : run(R16{}, no, no);
+    return hl ? run(R16{}, yes, yes) : run(R16{}, yes, no);
   }
 }
 
@@ -940,7 +947,7 @@ cudaError_t launch_paged_rows(const PagedAttentionArgs &a, cudaStream_t s) {
   p.slots = reinterpret_cast<float *>(p.desc + 2 * decode_ctas());
   // rows of a request and KV head that go through its tokens together; more of them are further units
   const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv);
-  const int rg = rows <= 4 ? 4 : rows <= 8 || a.dtype != TQ_BF16 || a.kq.d == 256 ? 8 : 16;
+  const int rg = rows <= 4 ? 4 : rows <= 8 || a.kq.d == 256 ? 8 : 16;
   const int unit_rows = a.kq.d == 256 ? Cfg<256>::kUnitRows : Cfg<128>::kUnitRows;
   p.groups = (int)((rows < unit_rows ? rows + rg - 1 : unit_rows) / rg);
   return a.kq.d == 64 ? run_d<64>(p, rg, s) : a.kq.d == 128 ? run_d<128>(p, rg, s) : run_d<256>(p, rg, s);

@@ -548,6 +548,17 @@ def test_ragged_rows_of_256(G, qs, kv, window, dtype):
         check_attention(p, causal=False)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("G,qs", [(1, [40, 33, 1]), (4, [10, 1, 9]), (8, [5, 5, 2]), (6, [8, 7, 0])])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_two_units(d, G, qs, dtype):
+    """Around the most rows that the small tiles take: more than one unit a request and head, and just beyond."""
+    p = paged_problem(d + G, qs, [300, 1000, 41], 2 * G, 2, d, 16, dtype)
+    poison_unseen(p[3], p[4], p[5], p[6])
+    check_attention(p)
+    check_attention(p, window=29)
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("qs,kv", [([1], [1]), ([1], [40]), ([70], [70]), ([1] * 300, [(17 * i) % 90 for i in range(300)]),
                                    ([40] + [1] * 20, [40] + [3000] + [5] * 19)])
