@@ -69,7 +69,8 @@ constexpr int kStages = 2;               // a warp's steps in shared memory: one
 
 template <int D>
 struct Cfg {
-  // 168 registers a thread; 16 warps of 128 took 207 us where 12 take 198 (d = 128)
+  // 168 registers a thread; 16 warps of 128 took 207 us where 12 take 198 (d = 128).  For d = 256 the sums, the query
+  // operands and the ring are twice as large: 8 warps of 255 registers
   static constexpr int kWarps = D == 256 ? 8 : 12;
   static constexpr int kMaxRows = D == 256 ? 8 : 16;    // query rows of a group of warps
   static constexpr int kUnitRows = D == 256 ? 16 : 32;  // of a unit
@@ -79,7 +80,8 @@ struct Cfg {
   static constexpr int kStepBytes = kStep * D + 2 * kStep * 4;
   static constexpr int kRing = kStages * kStepBytes;
   // rings above the tables (the partial sums reuse the space), the rest below
-  static constexpr int kHigh = (227 * 1024 - (int)kPartAddr) / kRing < kWarps ? (227 * 1024 - (int)kPartAddr) / kRing : kWarps;
+  static constexpr int kFit = (227 * 1024 - (int)kPartAddr) / kRing;
+  static constexpr int kHigh = kFit < kWarps ? kFit : kWarps;
 };
 
 // Shared memory below the tables.
@@ -89,7 +91,7 @@ struct Low {
   int64_t warp[Cfg<D>::kWarps];
   alignas(16) __half q[2][Cfg<D>::kUnitRows][D + 32];  // operand columns: hi of each row, lo of each row (q_place)
   float f[Cfg<D>::kUnitRows];                          // logit factor of each row
-  int see_lo[Cfg<D>::kUnitRows], see_hi[Cfg<D>::kUnitRows];    // the tokens that each row sees
+  int see_lo[Cfg<D>::kUnitRows], see_hi[Cfg<D>::kUnitRows];  // the tokens that each row sees
   float m[Cfg<D>::kWarps][Cfg<D>::kMaxRows], l[Cfg<D>::kWarps][Cfg<D>::kMaxRows];
   float scale[2];                  // what the tables' values are to be divided by
   unsigned key[2];
@@ -99,7 +101,8 @@ struct Low {
 
 template <int D>
 __host__ __device__ constexpr uint32_t smem_end() {
-  constexpr uint32_t parts = Cfg<D>::kWarps * Cfg<D>::kMaxRows * Cfg<D>::kPitch * 4, rings = Cfg<D>::kHigh * Cfg<D>::kRing;
+  constexpr uint32_t parts = Cfg<D>::kWarps * Cfg<D>::kMaxRows * Cfg<D>::kPitch * 4;
+  constexpr uint32_t rings = Cfg<D>::kHigh * Cfg<D>::kRing;
   static_assert(kPartAddr + (parts > rings ? parts : rings) <= 227 * 1024, "");
   return kPartAddr + (parts > rings ? parts : rings);
 }
@@ -108,8 +111,8 @@ struct RowsParams {
   PagedAttentionArgs a;
   int groups;       // warps are in so many groups of 4, 8 or 16 query rows, which go through the same steps
   float *slots;     // [2 * ctas][kUnitRows][D + 2]: sums, then M and L
-  int4 *desc;       // [2 * ctas]: {pieces, rows, first row, head}, {first query row, what the values' table is to be divided
-                    // by} of the unit that starts last in a range
+  int4 *desc;       // [2 * ctas]: {pieces, rows, first row, head}, {first query row, what the values' table is to be
+                    // divided by} of the unit that starts last in a range
   unsigned *faults;
 };
 
@@ -258,7 +261,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
   const int G = a.Hq / a.Hkv, c = blockIdx.x;
   const int groups = MULTI ? p.groups : 1;
   const int RT = RG * groups, WG = W / groups;         // rows of a unit, warps of a group
-  const int group = MULTI ? warp / WG : 0, wg = warp - group * WG, gr = RG * group;  // the warp's group, place in it, first row
+  // the warp's group, its place there, the group's first row
+  const int group = MULTI ? warp / WG : 0, wg = warp - group * WG, gr = RG * group;
   const int cost = kUnitCost / groups;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const uint32_t dyn = (uint32_t)__cvta_generic_to_shared(s_raw);
@@ -407,7 +411,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
             constexpr int TI = 1024 / D;                    // tokens of 32 lanes
             const uint32_t turn = D == 256 ? 64 * (i & 1) : 0;  // of k_place and v_place, TI i tokens on
             cp_async16(to + (k_to ^ turn) + hf * (8 * D) + 512 * i, ks + (UNIT ? 512 * i : TI * i * k_tok));
-            cp_async16(to + kStep * (D / 2) + (v_to ^ turn) + hf * (8 * D) + 512 * i, vs + (UNIT ? 512 * i : TI * i * v_tok));
+            cp_async16(to + kStep * (D / 2) + (v_to ^ turn) + hf * (8 * D) + 512 * i,
+                       vs + (UNIT ? 512 * i : TI * i * v_tok));
           }
           // lanes 0..15 the norms of K, the others those of V
           cp_async4(to + kStep * D + n_to + 64 * hf, n_lane + (UNIT || lane < 16 ? kr : vr));
@@ -606,7 +611,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
 #pragma unroll
           for (int ct = 0; ct < NC; ++ct)
 #pragma unroll
-            for (int o = 0; o < QS; ++o) qv[ct][o] = NC == 1 ? qb[NC == 1 ? o : 0][NC == 1 ? CW * r0 + w : 0] : load_q(o, ct, CW * r0 + w);
+            for (int o = 0; o < QS; ++o) {
+              if constexpr (NC == 1) qv[ct][o] = qb[o][CW * r0 + w];
+              else qv[ct][o] = load_q(o, ct, CW * r0 + w);
+            }
 #pragma unroll
           for (int x = 0; x < HV; ++x) {
             const int i = x;
@@ -681,7 +689,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
           const uint32_t o1 = ((c2[w] >> 4) & 0x0f0f0f0fu) | (c3[w] & 0xf0f0f0f0u);
           auto tile = [&](auto k) {
             constexpr int K = decltype(k)::value;
-            const uint32_t a0 = pair<K>(e0, vtab), a1 = pair<K>(o0, vtab), a2 = pair<K>(e1, vtab), a3 = pair<K>(o1, vtab);
+            const uint32_t a0 = pair<K>(e0, vtab), a1 = pair<K>(o0, vtab);
+            const uint32_t a2 = pair<K>(e1, vtab), a3 = pair<K>(o1, vtab);
 #pragma unroll
             for (int o = 0; o < QS; ++o)
 #pragma unroll
@@ -815,7 +824,9 @@ __global__ void __launch_bounds__(D * RT) paged_merge_kernel(const __grid_consta
   const float vs = __int_as_float(where.y);
   const int G = a.Hq / a.Hkv;
   // piece k's slot
-  auto slot = [&](int k) { return p.slots + (size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * Cfg<D>::kUnitRows * (D + 2) + r8 * (D + 2); };
+  auto slot = [&](int k) {
+    return p.slots + ((size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * Cfg<D>::kUnitRows + r8) * (D + 2);
+  };
   const int i = tid / D, k = tid % D;
   // the first pieces' sums are on their way while their factors are made
   constexpr int N = 20;
@@ -935,7 +946,8 @@ cudaError_t run_d(const RowsParams &p, int rg, cudaStream_t s) {
 
 size_t paged_rows_workspace(int d) {
   const size_t ctas = decode_ctas();
-  return 2 * ctas * sizeof(int4) + 2 * ctas * (d == 256 ? Cfg<256>::kUnitRows : Cfg<128>::kUnitRows) * (d + 2) * sizeof(float);
+  const int rows = d == 256 ? Cfg<256>::kUnitRows : Cfg<128>::kUnitRows;
+  return 2 * ctas * (sizeof(int4) + (size_t)rows * (d + 2) * sizeof(float));
 }
 
 cudaError_t launch_paged_rows(const PagedAttentionArgs &a, cudaStream_t s) {
