@@ -820,9 +820,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
 #pragma unroll
                 for (int e = 0; e < 8; ++e) most = __hmax2(most, *reinterpret_cast<const __half2 *>(to + e));
               });
-              // a reference that has just moved bounds the weights by 1 (and rounding)
+              // A reference that has just moved bounds the weights by 1 (and rounding).  A weight beyond fp32 whose value has
+              // no norm is inf * 0 here, which the maximum drops, so the sum is looked at too: behind a move it is at most
+              // 128 * 2^64, a value without a norm counting as one of 2^-64.
               const __half2 wide = __half2half2(__float2half(16384.f));
-              if (again || !__any_sync(dev::kFull, !__hbgt2(wide, most))) break;
+              if (again || !__any_sync(dev::kFull, !__hbgt2(wide, most) || sum[0] + sum[1] > 0x1p80f)) break;
               again = true;
             }
 #pragma unroll
