@@ -416,9 +416,9 @@ tq_status tq_paged_dequant(const tq_quantizer *q, const tq_cache_view *cache, in
  * and j > p - window.  Query head hq reads kv head hq / (Hq / Hkv).  Logits
  * are softmax_scale * <q, k_hat>; out: [T][Hq][d] contiguous, q's dtype; lse:
  * optional [T][Hq] fp32, the natural logarithm of the softmax's sum.  A row
- * that sees no token gets zeros (lse -inf); rows behind cu_q[R] are left as
- * they were.  max_q: an upper bound of the requests' row counts; it sizes the
- * work and never changes which rows are computed.
+ * that sees no token, or only logits of -inf, gets zeros (lse -inf); rows
+ * behind cu_q[R] are left as they were.  max_q: an upper bound of the requests'
+ * row counts; it sizes the work and never changes which rows are computed.
  * d is 64, 128 or 256, page_size a multiple of 16, R < 2^24.
  * workspace: DEVICE, at least tq_paged_attention_workspace_bytes(...) bytes,
  * 16-byte aligned, else TQ_EWORKSPACE; calls that may overlap on the GPU need

@@ -22,6 +22,13 @@ __device__ __forceinline__ float log2_approx(float x) {
   return y;
 }
 
+// log2 of a value norm as it counts where the softmax reference is chosen: at least -64; an infinite one, whose
+// product is infinite whatever the weight, does not count, so the other weights and their sum stay what they are.
+__device__ __forceinline__ float value_log2(float norm) {
+  const float x = log2_approx(norm);
+  return x < INFINITY ? fmaxf(x, -64.f) : -64.f;
+}
+
 // Scale of a table of fp16 levels.  The 16 levels c_k, rounded to fp16 once,
 // would be a fixed error of up to 2^-11 in every score and value; a factor s in
 // [1, 2) moves them to where fp16 holds them best.  What counts is the error

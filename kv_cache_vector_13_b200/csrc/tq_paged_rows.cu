@@ -546,7 +546,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
         for (int o = 0; o < 2; ++o) {
           float m = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) m = fmaxf(m, seen[i][o] ? s[i][o] + lv[i] : -INFINITY);
+          for (int i = 0; i < 4; ++i)  // an infinite value norm brings every step here, and does not count (value_log2)
+            m = fmaxf(m, seen[i][o] ? s[i][o] + (lv[i] < INFINITY ? lv[i] : -64.f) : -INFINITY);
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(dev::kFull, m, x));
           m = fmaxf(M[CT][o], m);

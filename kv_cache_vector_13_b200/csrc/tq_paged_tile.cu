@@ -253,7 +253,7 @@ struct Low {
   uint64_t k_full[2], v_full[2], k_free, v_free, n_full[kNormBufs], s_full[2], o_fin[2];
   uint32_t tmem, pad;
   Piece piece;
-  // of a block's tokens: ||k||, ||v||, max(log2 ||v||, -64), and whether they have a record
+  // of a block's tokens: ||k||, ||v||, value_log2 of it, and whether they have a record
   alignas(16) float kn[kNormBufs][kBlk], vn[kNormBufs][kBlk], lv[kNormBufs][kBlk];
   alignas(16) uint32_t valid[kNormBufs][kBlk / 32];
   float f[256];          // score factors of the rows
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
           if (lane == 0) sm.valid[nb][wq] = ok;
         } else {
           sm.vn[nb][32 * wq + lane] = norm;
-          sm.lv[nb][32 * wq + lane] = fmaxf(log2_approx(norm), -64.f);
+          sm.lv[nb][32 * wq + lane] = value_log2(norm);
         }
         arrive(bar(sm.n_full[nb]));
       };

@@ -76,3 +76,17 @@ def test_large_logits_of_values_without_a_norm(d, n, dtype, R, size, zeros):
         kc.norms[page, 0, j % 16] = key.norms[0, 0, 0]
         vc.norms[page, 0, j % 16] = 0
     check_repeated(p, R, least=460 * 2.0 ** -89 * float(vc.norms.max()))
+
+
+@pytest.mark.parametrize("R", [1, 200])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d,n", [(128, 1), (128, 8), (128, 24), (128, 45), (128, 100), (64, 100), (256, 20)])
+@pytest.mark.parametrize("at", [3, 290, 459])
+def test_an_infinite_value_norm_reaches_its_rows_only(d, n, dtype, R, at):
+    """A value row that overflowed before it was stored: NaN in every row that
+    sees it, as the definition has it, and their lse as it would be without."""
+    p = paged_problem(n + d, [n], [460], 4, 2, d, 16, dtype)
+    p[4].norms[p[5][0, at // 16].long(), 1, at % 16] = float("inf")
+    finite = np.ones((n, 4), bool)
+    finite[:, 2:] = (460 - n + np.arange(n) < at)[:, None]
+    check_repeated(p, R, finite)
