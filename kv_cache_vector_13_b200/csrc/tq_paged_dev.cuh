@@ -22,6 +22,11 @@ __device__ __forceinline__ float log2_approx(float x) {
   return y;
 }
 
+// The first token that position p sees: p may be far below 0 and the window as large as an int.
+__device__ __forceinline__ int window_start(int p, int window) {
+  return window > 0 ? max(max(p + 1, 0) - window, 0) : 0;
+}
+
 // log2 of a value norm as it counts where the softmax reference is chosen: at least -64; an infinite one, whose
 // product is infinite whatever the weight, does not count, so the other weights and their sum stay what they are.
 __device__ __forceinline__ float value_log2(float norm) {

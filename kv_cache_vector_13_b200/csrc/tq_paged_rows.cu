@@ -138,7 +138,7 @@ __device__ __forceinline__ Req load_req(const PagedAttentionArgs &a, int r, int 
     q.kv = cap;
   }
   q.tiles = (q.n * (a.Hq / a.Hkv) + rows_per_tile - 1) / rows_per_tile;
-  q.first = a.window > 0 ? max(q.kv - q.n + 1 - a.window, 0) : 0;
+  q.first = window_start(q.kv - q.n, a.window);
   q.lo = q.first / kStep;
   // a request that sees nothing still has one (empty) step, which writes its zeros
   q.hi = max((q.kv + kStep - 1) / kStep, q.lo + 1);
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
         if (i < nrows) {
           const int pos = req.kv - req.n + (row0 + i) / G;
           hi = a.causal ? max(pos + 1, 0) : req.kv;
-          lo = a.window > 0 ? max(pos + 1 - a.window, 0) : 0;
+          lo = window_start(pos, a.window);
         }
         s_f[i] = kscale / f;
         sm.see_lo[i] = lo;
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
     const int first_pos = req.kv - req.n + (row0 + gr) / G,
               last_pos = req.kv - req.n + (row0 + gr + mine_rows - 1) / G;
     const int full_hi = a.causal ? max(first_pos + 1, 0) : req.kv;
-    const int full_lo = a.window > 0 ? max(last_pos + 1 - a.window, 0) : 0;
+    const int full_lo = window_start(last_pos, a.window);
 
     float acc[NC][MV][4];
 #pragma unroll

@@ -104,7 +104,7 @@ __device__ __forceinline__ void tile_blocks(const PagedAttentionArgs &a, const R
   const int G = a.Hq / a.Hkv;
   const int p0 = q.kv - q.n + i * rt / G, p1 = q.kv - q.n + (min((i + 1) * rt, q.n * G) - 1) / G;
   const int hi = a.causal ? max(p1 + 1, 0) : q.kv;
-  first = a.window > 0 ? max(p0 + 1 - a.window, 0) : 0;
+  first = window_start(p0, a.window);
   b0 = first / kBlk;
   b1 = max((hi + kBlk - 1) / kBlk, b0 + 1);
 }
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
       if (live) {
         const int pos = q.kv - q.n + (q.row0 + i) / G;
         see_hi = a.causal ? max(pos + 1, 0) : q.kv;
-        see_lo = a.window > 0 ? max(pos + 1 - a.window, 0) : 0;
+        see_lo = window_start(pos, a.window);
       }
       const float f = sm.f[i];
       float M = -FLT_MAX, l = 0.f;

@@ -90,3 +90,11 @@ def test_an_infinite_value_norm_reaches_its_rows_only(d, n, dtype, R, at):
     finite = np.ones((n, 4), bool)
     finite[:, 2:] = (460 - n + np.arange(n) < at)[:, None]
     check_repeated(p, R, finite)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 6])
+@pytest.mark.parametrize("d,qs,kv", [(128, [8, 1], [3, 40]), (128, [70, 5], [20, 300]), (64, [300], [7]), (256, [30], [5])])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_a_window_wider_than_any_cache(d, qs, kv, dtype, window):
+    """More query rows than cached tokens: their positions start below 0."""
+    check_attention(paged_problem(d, qs, kv, 4, 2, d, 16, dtype), window=window)
