@@ -92,6 +92,7 @@ class Quantizer:
                                 L.TQ_ROT_DENSE if rotation == "dense" else L.TQ_ROT_HADAMARD,
                                 _ptr(self.centroids), _ptr(self.thresholds), _ptr(self.signs), _ptr(self.S),
                                 _ptr(self.rot), _ptr(self.channels))
+        self._ref = ctypes.byref(self._c)
 
     @property
     def prod(self) -> bool:
@@ -114,7 +115,7 @@ class Quantizer:
         return self._c
 
     def c_ref(self):
-        return ctypes.byref(self._c)
+        return self._ref
 
 
 @dataclass
@@ -131,7 +132,9 @@ class PackedCache:
 
     def view(self) -> L.TqCacheView:
         # built once per (arrays, layout): a decode step passes the same views
-        key = (_ptr(self.codes), _ptr(self.qjl), _ptr(self.norms), _ptr(self.rnorms), self.norms.stride())
+        c, q, n, r = self.codes, self.qjl, self.norms, self.rnorms
+        key = (None if c is None else c.data_ptr(), None if q is None else q.data_ptr(), n.data_ptr(),
+               None if r is None else r.data_ptr(), n.stride())
         cached = self.__dict__.get("_view")
         if cached is not None and cached[0] == key:
             return cached[1]
@@ -139,13 +142,15 @@ class PackedCache:
         for t in (self.codes, self.qjl, self.rnorms):
             if t is not None:
                 w = t.shape[3] if t.dim() == 4 else 1
-                assert t.stride()[:3] == (sb * w, sh * w, sn * w), "all arrays must share one record layout"
+                assert t.stride()[:3] == (sb * w, sh * w, sn * w) and (t.dim() < 4 or w <= 1 or t.stride(3) == 1), \
+                    "all arrays must share one record layout"
         v = L.TqCacheView(key[0], key[1], key[2], key[3], sb, sh, sn)
-        self.__dict__["_view"] = (key, v)
+        self.__dict__["_view"] = (key, v, ctypes.byref(v))
         return v
 
     def c_ref(self):
-        return ctypes.byref(self.view())
+        self.view()
+        return self.__dict__["_view"][2]
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in (self.codes, self.qjl, self.norms, self.rnorms)
@@ -392,9 +397,16 @@ def _check(device: int, dtype, **ts) -> None:
             raise AssertionError(f"{name}: a contiguous {dtype} tensor on device {device}, got {t.dtype} on {t.device}")
 
 
-def _check_caches(device: int, kq: Quantizer, vq: Quantizer, kcache, vcache) -> None:
-    for t in (kcache.norms, vcache.norms, kq.signs, vq.signs):
-        assert t.get_device() == device, f"caches and quantizers must be on device {device}"
+def _check_cache(device: int, qz: Quantizer, cache: PackedCache, shape) -> None:
+    """A cache of this quantizer's records, norms of this shape, on this
+    device: the kernels take the records' size from the quantizer alone."""
+    codes, norms = cache.codes, cache.norms
+    assert norms.dtype is torch.float32 and codes is not None and codes.dtype is torch.uint8, \
+        "a cache has fp32 norms and uint8 codes"
+    assert codes.shape == (*shape, qz.code_bytes), \
+        f"codes {tuple(codes.shape)} are not those of {tuple(shape)} records of this quantizer"
+    assert norms.get_device() == device and codes.get_device() == device and qz.signs.get_device() == device, \
+        f"caches and quantizers must be on device {device}"
 
 
 def _check_table(device: int, table: torch.Tensor, R: int):
@@ -495,9 +507,10 @@ def paged_append(kq: Quantizer, vq: Quantizer, k: torch.Tensor, v: torch.Tensor,
     assert d == kq.d and v.shape == k.shape and v.dtype is dt and dt in _DTYPES
     assert v.get_device() == dev and slots.shape == (T,)
     _check(dev, torch.int64, slots=slots)
-    n_pages, H, P = kcache.norms.shape
-    assert H == Hkv and vcache.norms.shape == kcache.norms.shape
-    _check_caches(dev, kq, vq, kcache, vcache)
+    n_pages, H, P = shape = kcache.norms.shape
+    assert H == Hkv and vcache.norms.shape == shape
+    _check_cache(dev, kq, kcache, shape)
+    _check_cache(dev, vq, vcache, shape)
     pos_stride, rp, pp = 0, None, None
     if rope is not None:
         assert positions is not None and positions.dtype is torch.int32 and positions.get_device() == dev
@@ -526,10 +539,10 @@ def paged_dequant(qz: Quantizer, cache: PackedCache, slots: torch.Tensor, dtype=
                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """tq_paged_dequant: the vectors of the records at slots [T] (int64; -1
     gives zeros) as [T, H, d] in dtype."""
-    n_pages, H, P = cache.norms.shape
+    n_pages, H, P = shape = cache.norms.shape
     (T,), dev = slots.shape, cache.norms.get_device()
     _check(dev, torch.int64, slots=slots)
-    _check_caches(dev, qz, qz, cache, cache)
+    _check_cache(dev, qz, cache, shape)
     if out is None:
         out = torch.empty((T, H, qz.d), dtype=dtype, device=cache.norms.device)
     assert out.shape == (T, H, qz.d) and out.dtype in _DTYPES
@@ -565,13 +578,14 @@ class PagedAttention:
         1 without cu_q, else T).  Returns out [T, Hq, d] in q's dtype; lse
         [T, Hq] (fp32), if given, gets the logarithm of the softmax's sums."""
         (T, Hq, d), (R,), dt, dev = q.shape, kv_lens.shape, q.dtype, self.device
-        n_pages, Hkv, P = kcache.norms.shape
-        assert (Hq, Hkv, d) == (self.Hq, self.Hkv, self.kq.d) and vcache.norms.shape == kcache.norms.shape
+        n_pages, Hkv, P = shape = kcache.norms.shape
+        assert (Hq, Hkv, d) == (self.Hq, self.Hkv, self.kq.d) and vcache.norms.shape == shape
         assert dt in _DTYPES and q.get_device() == dev
         assert R <= self.max_requests and T <= self.max_tokens, "more requests or rows than the workspace is for"
         assert cu_q is None or cu_q.shape == (R + 1,)
         _check(dev, torch.int32, kv_lens=kv_lens, cu_q=cu_q)
-        _check_caches(dev, self.kq, self.vq, kcache, vcache)
+        _check_cache(dev, self.kq, kcache, shape)
+        _check_cache(dev, self.vq, vcache, shape)
         stride, width = _check_table(dev, block_table, R)
         if max_q is None:
             max_q = 1 if cu_q is None else max(T, 1)
