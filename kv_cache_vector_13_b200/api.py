@@ -371,6 +371,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 def _call(device: int, stream, fn, *args) -> None:
     """fn(*args, stream) with `device` current, on `stream` or that device's
     current one."""
+    assert device >= 0, "the tensors of a paged call are on a CUDA device"
     s = _raw_stream(device) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == device:
         status = fn(*args, s)

@@ -21,6 +21,7 @@ def calls(kq, vq, kc, vc, bad_k):
     slots = torch.zeros(4, dtype=torch.int64)
     op = object.__new__(api.PagedAttention)  # without a workspace, which needs a GPU
     op.kq, op.vq, op.Hq, op.Hkv, op.max_requests, op.max_tokens, op.device = kq, vq, 2, 2, 4, 4, -1
+    op._ws, op.ws_bytes = 0, 0
     yield lambda: api.paged_append(kq, vq, k, k, kc, vc, slots)
     yield lambda: api.paged_dequant(*((kq, kc) if bad_k else (vq, vc)), slots)
     yield lambda: op(k.bfloat16(), kc, vc, torch.zeros((4, 2), dtype=torch.int32), torch.ones(4, dtype=torch.int32))
@@ -50,3 +51,15 @@ def test_caches_that_are_not_the_quantizers_are_refused(bad):
         for call in calls(kq, vq, kx, vx, bad_k):
             with pytest.raises(AssertionError, match="fp32 norms and uint8 codes|are not those of|share one record layout"):
                 call()
+
+
+def test_tensors_of_the_host_are_refused():
+    """Host addresses may not reach a launch, whatever GPU is there."""
+    kq, vq = quantizer(), quantizer(seed_rot=1)
+    for bad_k in (True, False):
+        for call in calls(kq, vq, cache(kq), cache(vq), bad_k):
+            with pytest.raises(AssertionError, match="CUDA device"):
+                call()
+    i32 = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(AssertionError, match="CUDA device"):
+        api.PagePlanner(2, 16, 8, device="cpu")(i32, i32, i32, i32[:1], torch.zeros((2, 4), dtype=torch.int32))
