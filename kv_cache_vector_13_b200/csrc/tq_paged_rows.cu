@@ -519,7 +519,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
         for (int e = 0; e < 4; ++e) acc[ct][j][e] = 0.f;
 
     // The running softmax of the lane's rows over its tokens 8 i + g (value [i][o]: row o): scores in, weights
-    // times value norms out.  M is a reference that moves only when one of them would pass 2^14 (fp16 ends at 2^16).
+    // times value norms out.  M is a reference that moves only when one of them would pass 2^15 (fp16 ends at 2^16),
+    // and then to kRoom below the largest.
     auto soft = [&](auto edge, auto tile, int t0, uint32_t halves, float (&t)[4][2], const float (&kn)[4],
                     const float (&vn)[4], const float (&lv)[4]) {
       constexpr bool EDGE = decltype(edge)::value;
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(t[i][0], t[i][1]) + lv[i]);
-      if (__any_sync(dev::kFull, mx > 14.f)) {
+      if (__any_sync(dev::kFull, mx > kMost)) {
         float r2[2];
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
             m = fmaxf(m, seen[i][o] ? s[i][o] + (lv[i] < INFINITY ? lv[i] : -64.f) : -INFINITY);
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(dev::kFull, m, x));
-          m = fmaxf(M[CT][o], m);
+          m = fmaxf(M[CT][o], m - kRoom);
           r2[o] = exp2f(M[CT][o] - m);
           M[CT][o] = m;
           l[CT][o] *= r2[o];

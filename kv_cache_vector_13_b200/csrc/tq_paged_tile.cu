@@ -774,9 +774,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
             }
           }
         };
-        // moves the reference M to the block's largest value if that is above it
+        // moves the reference M to that room below the block's largest value if that is above it
         auto move = [&](float mx) {
-          const float m2 = fmaxf(M, mx), r2 = exp2f(M - m2);
+          const float m2 = fmaxf(M, mx - (HL ? kRoom : kRoomOnce)), r2 = exp2f(M - m2);
           M = m2;
           l *= r2;
           if (k > 0) {  // the scores' barrier says that the products before them are done, those into O too
@@ -791,14 +791,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
             }
           }
         };
-        // M moves only when a weight times its norm would pass 2^14 (fp16 ends at 2^16): with HL that is looked for before the
+        // M moves only when a weight times its norm would pass 2^15 (fp16 ends at 2^16): with HL that is looked for before the
         // weights, which take the scores' place at once; else the weights are kept in registers, and where one
         // is too large they are made again
         auto item = [&](auto edge) {
           float sum[2] = {0.f, 0.f};
           if constexpr (HL) {
             const float mx = top(edge);
-            if (__any_sync(dev::kFull, mx > M + 14.f)) move(mx);
+            if (__any_sync(dev::kFull, mx > M + kMost)) move(mx);
             uint32_t w[16], wl[16];
             runs([&](int c8, const uint32_t (&s)[16]) {
               weights(edge, c8, s, sum, w + 8 * (c8 & 1), wl + 8 * (c8 & 1));
@@ -820,10 +820,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
 #pragma unroll
                 for (int e = 0; e < 8; ++e) most = __hmax2(most, *reinterpret_cast<const __half2 *>(to + e));
               });
-              // A reference that has just moved bounds the weights by 1 (and rounding).  A weight beyond fp32 whose value has
+              // A reference that has just moved bounds the weights by 2 (and rounding).  A weight beyond fp32 whose value has
               // no norm is inf * 0 here, which the maximum drops, so the sum is looked at too: behind a move it is at most
-              // 128 * 2^64, a value without a norm counting as one of 2^-64.
-              const __half2 wide = __half2half2(__float2half(16384.f));
+              // 128 * 2^65, a value without a norm counting as one of 2^-64.
+              const __half2 wide = __half2half2(__float2half(1 << (int)kMost));
               if (again || !__any_sync(dev::kFull, !__hbgt2(wide, most) || sum[0] + sum[1] > 0x1p80f)) break;
               again = true;
             }

@@ -98,3 +98,70 @@ def test_an_infinite_value_norm_reaches_its_rows_only(d, n, dtype, R, at):
 def test_a_window_wider_than_any_cache(d, qs, kv, dtype, window):
     """More query rows than cached tokens: their positions start below 0."""
     check_attention(paged_problem(d, qs, kv, 4, 2, d, 16, dtype), window=window)
+
+
+@pytest.mark.parametrize("apart", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d,n", [(128, 1), (128, 8), (128, 16), (128, 40), (128, 60), (128, 160), (64, 1), (64, 60), (256, 8)])
+def test_many_small_weights_beside_a_large_one(d, n, dtype, apart):
+    """Tokens in the first runs of 32 (small tiles: 12, one a run; else one a
+    block of 128 in two) whose weight is 2^25.2 times that of each of the many
+    others, which together carry about a fiftieth of the output (apart: their
+    value's coordinates are of the largest level, the large token's of the
+    smallest) or a hundredth (values of one kind, up to three million tokens).
+    148 equal requests, so a CTA has a whole one.
+
+    The relative 2-norm error: the levels' rounding 2^-11; for bf16 rows and
+    weights 2^-11 each, rows behind the weights' logit of 17.5 for the share s
+    of the small ones alone (the large ones are alike); the output's half step;
+    half of fp16's smallest step, 2^-25, a weight of 2^-25.2 of the largest:
+    that is kept at 2^8, so 2^-7.8 of s (were it kept at 1, all of s would be
+    lost; for bf16 on the large tiles it is kept at 2, and the small weights,
+    0.87 of the smallest step, round to it: 0.15 of s).  The products are summed in 32 bits: each may be cut
+    below 2^-24 of the sum it goes into, which takes the products of a warp's
+    tokens (one of 12, or 6 or 8) or a set's (all, or every other block's),
+    two a token where weights are pairs."""
+    kq, vq = quantizers(d)
+    pairs, large = dtype == torch.float16, n > (48 if dtype == torch.float16 else 40)
+    g, R, P, pages = gen(d + n), 148, 384, (200 if large else 1000) if apart else 8000
+    x = torch.randn((2, 2, 1, 1, d), generator=g, device=DEV)
+    q = torch.randn((1, 1, d), generator=g, device=DEV).to(dtype)
+    # the large token's key lies along the query; the others' have no norm, so their logit is 0
+    kc = api.encode(kq, q.float()[None].expand(2, 1, P, d).contiguous())
+    vc = api.encode(vq, x[1].expand(2, 1, P, d).contiguous())
+    big = api.encode(vq, x[0, :1])
+    if apart:  # levels 7 and 8 are the two next to 0, 0 and 15 the outermost
+        sign = torch.randint(0, 2, (d,), generator=g, device=DEV).to(torch.uint8)
+        pack = lambda c: (c[0::2] | c[1::2] << 4)  # noqa: E731
+        big.codes[:], vc.codes[:] = pack(7 + sign), pack(15 * sign.flip(0))
+        big.norms.fill_(3.0)
+        vc.norms.fill_(3.0)
+    kc.norms.zero_()
+    ok, ov = oracle_twin(kq), oracle_twin(vq)
+    qr = rotate64(host(q)[0, 0].astype(np.float64), ok.signs.astype(np.float64))
+    unit = unpacked64(ok, host(kc.codes[0, 0, :1]), np.ones(1))[0] @ qr / math.sqrt(d)
+    norm = np.float32(25.2 * math.log(2) / unit)
+    at = torch.tensor([0, 128] if large and apart else range(0, P, 32), device=DEV)
+    kc.norms[0, 0, at] = float(norm)
+    vc.codes[0, 0, at] = big.codes[0, 0, 0]
+    vc.norms[0, 0, at] = big.norms[0, 0, 0]
+    big_v = unpacked64(ov, host(big.codes)[0, 0], host(big.norms)[0, 0])[0]
+    small_v = unpacked64(ov, host(vc.codes[1, 0, :1]), host(vc.norms[1, 0, :1]))[0]
+    count, w = P * pages - len(at), len(at) * math.exp(float(norm) * unit)
+    want = rotate64((w * big_v + count * small_v) / (w + count), 1.0) * ov.signs
+    s = count * np.linalg.norm(small_v) / np.linalg.norm(w * big_v + count * small_v)
+    table = torch.ones((1, pages), dtype=torch.int32, device=DEV)
+    table[0, 0] = 0
+    lens = torch.full((R,), P * pages, dtype=torch.int32, device=DEV)
+    cu = torch.arange(R + 1, dtype=torch.int32, device=DEV) * n
+    op = api.PagedAttention(kq, vq, 1, 1, R, R * n, device=DEV)
+    out = op(q.repeat(R * n, 1, 1), kc, vc, table.expand(R, pages).contiguous(), lens, cu_q=cu, max_q=n, causal=False)
+    api.check()
+    off = np.linalg.norm(host(out)[:, 0].astype(np.float64) - want, axis=-1) / np.linalg.norm(want)
+    once = 0 if pairs or n <= 4 else 2.0 ** -11
+    sets = (1 if n > 128 and not pairs else 2) if large else 8 if d == 256 else 6 if n > 16 else 12
+    sums = P * pages / sets * (2 if pairs and n > 4 else 1) * 2.0 ** -24
+    step = 2.0 ** 0.2 - 0.999 if large and not pairs else 2.0 ** -7.8
+    bar = 2.0 ** -11 + torch.finfo(dtype).eps / 2 + once + s * (2 * 17.5 * 2.0 ** -10 + step) + sums
+    assert off.max() <= bar, (off.max(), bar, s)
+    assert not apart or bar < 0.98 * s  # a bar that the loss of the small ones would not pass
