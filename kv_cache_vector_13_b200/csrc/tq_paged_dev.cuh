@@ -30,6 +30,9 @@ __device__ __forceinline__ float log2_approx(float x) {
 // rows take 1509 us with room 8, 1381 with 1 as without.  There it is 1, next to what the tensor cores' sums cut (2^-24).
 constexpr float kMost = 15.f, kRoom = 8.f, kRoomOnce = 1.f;
 
+// Runs of n tokens that hold the first `tokens` (which may be next to 2^31).
+__device__ __forceinline__ int runs(int tokens, int n) { return (int)(((unsigned)tokens + n - 1) / n); }
+
 // The first token that position p sees: p may be far below 0 and the window as large as an int.
 __device__ __forceinline__ int window_start(int p, int window) {
   return window > 0 ? max(max(p + 1, 0) - window, 0) : 0;

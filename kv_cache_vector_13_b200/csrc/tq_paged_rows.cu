@@ -141,7 +141,7 @@ __device__ __forceinline__ Req load_req(const PagedAttentionArgs &a, int r, int 
   q.first = window_start(q.kv - q.n, a.window);
   q.lo = q.first / kStep;
   // a request that sees nothing still has one (empty) step, which writes its zeros
-  q.hi = max((q.kv + kStep - 1) / kStep, q.lo + 1);
+  q.hi = max(runs(q.kv, kStep), q.lo + 1);
   return q;
 }
 
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) paged_rows_kernel(const _
         vn[i] = lds_f32(from + kStep * D + 128 + 4 * (8 * i + g));
         lv[i] = fmaxf(log2_approx(vn[i]), -64.f);
       }
-      const bool edge = t0 + kStep > full_hi || t0 < full_lo || halves != 3;
+      const bool edge = (unsigned)t0 + kStep > (unsigned)full_hi || t0 < full_lo || halves != 3;
       uint32_t pb[NC][QS][4];
       auto weights = [&](auto tile) {
         constexpr int CT = decltype(tile)::value;

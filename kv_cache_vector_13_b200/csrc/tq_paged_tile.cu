@@ -106,7 +106,7 @@ __device__ __forceinline__ void tile_blocks(const PagedAttentionArgs &a, const R
   const int hi = a.causal ? max(p1 + 1, 0) : q.kv;
   first = window_start(p0, a.window);
   b0 = first / kBlk;
-  b1 = max((hi + kBlk - 1) / kBlk, b0 + 1);
+  b1 = max(runs(hi, kBlk), b0 + 1);
 }
 
 // ------------------------------------------------- query rows and schedule
@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         umma::fence_after();
         const uint4 vm = *reinterpret_cast<const uint4 *>(sm.valid[nb]);
         const uint32_t valid[4] = {vm.x, vm.y, vm.z, vm.w};
-        const bool whole = see_lo <= j0 && see_hi >= j0 + kBlk && (vm.x & vm.y & vm.z & vm.w) == ~0u;
+        const bool whole = see_lo <= j0 && (unsigned)see_hi >= (unsigned)j0 + kBlk && (vm.x & vm.y & vm.z & vm.w) == ~0u;
         const float *kns = sm.kn[nb], *vns = sm.vn[nb], *lvs = sm.lv[nb];
         auto mask = [&](int r) {  // tokens of run r (32 columns) that the row sees
           const int lo = max(see_lo - j0 - 32 * r, 0), hi = min(see_hi - j0 - 32 * r, 32);

@@ -165,3 +165,29 @@ def test_many_small_weights_beside_a_large_one(d, n, dtype, apart):
     bar = 2.0 ** -11 + torch.finfo(dtype).eps / 2 + once + s * (2 * 17.5 * 2.0 ** -10 + step) + sums
     assert off.max() <= bar, (off.max(), bar, s)
     assert not apart or bar < 0.98 * s  # a bar that the loss of the small ones would not pass
+
+
+@pytest.mark.parametrize("dtype,n", [(torch.bfloat16, 1), (torch.float16, 20), (torch.bfloat16, 60), (torch.float16, 60),
+                                     (torch.bfloat16, 150)])
+def test_the_longest_request(dtype, n):
+    """2^31 - 16 tokens: 262657 times the same page of 8176, so the output is
+    the page's own and its lse the page's plus log 262657.  The tensor cores'
+    32-bit sums cut each product below 2^-24 of the sum it goes into, so the
+    output may lose that for each of a warp's tokens (2^31 / 1776) or of a set's
+    (2^31 / 296, or / 148 where the sets split the rows), twice where weights
+    are pairs; the scalar sums of the weights lose at most 2^-24 in each of a
+    lane's 2^17.3 additions.  A length that wraps leaves an output several times
+    its own norm away."""
+    P, m = 8176, 262657
+    kq, vq, q, kc, vc, table, kv_lens, cu = paged_problem(n, [n], [P], 1, 1, 64, P, dtype, spare=0)
+    op = api.PagedAttention(kq, vq, 1, 1, 1, n, device=DEV)
+    lse, one_lse = torch.empty((n, 1), device=DEV), torch.empty((n, 1), device=DEV)
+    one = op(q, kc, vc, table, kv_lens, cu_q=cu, max_q=n, lse=one_lse, causal=False)
+    long = torch.full((1, m), int(table[0, 0]), dtype=torch.int32, device=DEV)
+    out = op(q, kc, vc, long, torch.full_like(kv_lens, P * m), cu_q=cu, max_q=n, lse=lse, causal=False)
+    api.check()
+    off = (out.float() - one.float()).norm(dim=-1) / one.float().norm(dim=-1)
+    tokens = 2 ** 31 / (888 if n == 20 else 1776 if n == 1 else 148 if n == 150 else 296)
+    bar = tokens * 2.0 ** -24 * (2 if dtype == torch.float16 and n > 4 else 1) + 2.0 ** -6
+    assert bool((off <= bar).all()), (off.max(), bar)
+    assert bool(((lse - one_lse - math.log(m)).abs() <= 2.0 ** -6).all())
