@@ -55,6 +55,11 @@ __device__ __forceinline__ void fwht_row(float (&a)[E], int t) {
   dev::fwht_local<E>(a);
 }
 
+// Neither a slot of the cache nor -1, which is none.
+__device__ __forceinline__ bool bad_slot(int64_t slot, int64_t n_slots) {
+  return (uint64_t)slot + 1 > (uint64_t)n_slots;
+}
+
 // The lane's signs of a rotation as +1 and -1.
 __device__ __forceinline__ void load_signs(const int8_t *signs, float (&s)[E]) {
 #pragma unroll
@@ -132,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, DT == TQ_F32 ? 2 : 3) paged_append_k
     if (k < ntok) {
       const int64_t slot = a.slots[tok0 + k];
       int64_t kr = -1, vr = -1;
-      if (slot >= a.n_slots) {
+      if (bad_slot(slot, a.n_slots)) {
         if (blockIdx.y == 0) atomicOr(p.faults, kFaultIndex);
       } else if (slot >= 0) {
         const int64_t page = slot / a.page_size, off = slot - page * a.page_size;
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) paged_dequant_kernel(ReadParams p) {
     dev::split_bhn(p.rows, row, none, tok, h);
     const int64_t slot = a.slots[tok];
     int64_t rec = -1;
-    if (slot >= a.n_slots) {
+    if (bad_slot(slot, a.n_slots)) {
       if (t == 0 && h == 0) atomicOr(p.faults, kFaultIndex);
     } else if (slot >= 0) {
       const int64_t page = p.small ? (int64_t)(((uint64_t)slot * p.page_mul) >> p.page_shift) : slot / a.page_size;

@@ -191,3 +191,30 @@ def test_the_longest_request(dtype, n):
     bar = tokens * 2.0 ** -24 * (2 if dtype == torch.float16 and n > 4 else 1) + 2.0 ** -6
     assert bool((off <= bar).all()), (off.max(), bar)
     assert bool(((lse - one_lse - math.log(m)).abs() <= 2.0 ** -6).all())
+
+
+def refused(match="outside its cache"):
+    with pytest.raises(L.TqError, match=match):
+        api.check()
+    api.check()  # the word is cleared
+
+
+@pytest.mark.parametrize("slot", [-2, -2 ** 31, -2 ** 63])
+def test_negative_slots_other_than_none_are_reported(slot):
+    kq, vq = quantizers(64)
+    kc, vc = (api.empty_cache(z, 2, 3, 16, device=DEV) for z in (kq, vq))
+    for c in (kc, vc):
+        c.codes.fill_(5)
+        c.norms.fill_(2.0)
+    k = torch.randn((3, 3, 64), generator=gen(1), device=DEV)
+    none, bad = (torch.tensor([7, s, 9], device=DEV) for s in (-1, slot))
+    api.paged_append(kq, vq, k, k, kc, vc, none)
+    want = api.paged_dequant(kq, kc, none)
+    api.check()
+    api.paged_append(kq, vq, k, k, kc, vc, bad)
+    refused()
+    got = api.paged_dequant(kq, kc, bad)
+    refused()
+    assert torch.equal(got, want) and bool((got[1] == 0).all())
+    touched = kc.norms != 2.0
+    assert int(touched.sum()) == 6 and bool(touched.view(-1, 16)[:3, [7, 9]].all())  # page 0, three heads
