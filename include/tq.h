@@ -354,10 +354,12 @@ int32_t tq_set_decode_feed(int32_t feed);
  *   n_free_out[1]         free pages left;
  *   block_table           the entries of the new pages, nothing else.
  * Once a request is refused for pages, so is every later one that needs any;
- * one that needs none is never refused for pages.  free_pages has free_cap
- * entries; *n_free (DEVICE) is clamped to 0..free_cap.  Outputs must not
- * alias inputs (block_table is both: its old pages are read).  R >= 0,
- * page_size >= 1, max_pages * page_size < 2^31, max_tokens < 2^31. */
+ * one that needs none is never refused for pages.  A token whose page is
+ * negative in the table or the free list has slot -1, and the next tq_check
+ * returns TQ_EINVAL.  free_pages has free_cap entries; *n_free (DEVICE) is
+ * clamped to 0..free_cap.  Outputs must not alias inputs (block_table is both:
+ * its old pages are read).  R >= 0, page_size >= 1, max_pages * page_size <
+ * 2^31, max_tokens < 2^31. */
 tq_status tq_page_plan(int32_t R, int32_t page_size, const int32_t *lens, const int32_t *new_lens,
                        const int32_t *free_pages, int64_t free_cap, const int32_t *n_free,
                        int32_t *block_table, int64_t table_stride, int32_t max_pages,

@@ -18,6 +18,7 @@ struct PagePlanArgs {
   int64_t max_tokens;
   int64_t *slots;
   int32_t *positions, *cu_new, *seq_lens, *status, *n_free_out;
+  unsigned *faults;       // the launcher's
 };
 
 struct PagedAppendArgs {

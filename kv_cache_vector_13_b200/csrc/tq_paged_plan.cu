@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(PagePlanArgs p) {
           id = row[page];
         }
         slot = id < 0 ? -1 : (int64_t)id * P + off;
+        if (id < 0) atomicOr(p.faults, kFaultIndex);  // an accepted token without a place
       }
       p.slots[t] = slot;
       p.positions[t] = (int32_t)pos;
@@ -193,7 +194,10 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(PagePlanArgs p) {
 
 cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t s) {
   const int64_t blocks = a.max_tokens > 0 ? (a.max_tokens + kTokens - 1) / kTokens : 1;
-  page_plan_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(a);
+  PagePlanArgs p = a;
+  const cudaError_t e = fault_word(&p.faults);
+  if (e != cudaSuccess) return e;
+  page_plan_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 

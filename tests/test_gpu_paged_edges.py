@@ -218,3 +218,22 @@ def test_negative_slots_other_than_none_are_reported(slot):
     assert torch.equal(got, want) and bool((got[1] == 0).all())
     touched = kc.norms != 2.0
     assert int(touched.sum()) == 6 and bool(touched.view(-1, 16)[:3, [7, 9]].all())  # page 0, three heads
+
+
+def test_a_plan_over_a_missing_page_is_reported():
+    """A request whose last page is begun but not in its table row: its tokens
+    there have no slot."""
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    for missing, slots in ((-1, [-1, -1, 16 * 9]), (3, [16 * 3 + 14, 16 * 3 + 15, 16 * 9])):
+        table = torch.full((2, 4), -1, dtype=torch.int32, device=DEV)
+        table[0, 0] = missing
+        p = api.PagePlanner(2, 16, 4, device=DEV)(i32(14, 0), i32(3, 1), i32(8, 9), i32(2), table)
+        if missing < 0:
+            refused()
+        else:
+            api.check()
+        assert p.slots.tolist() == slots + [16 * 8] and p.status.tolist() == [0, 0]
+    # a request that is refused, or adds nothing, reads no page
+    p = api.PagePlanner(2, 16, 40, device=DEV)(i32(14, 5), i32(40, 0), i32(8), i32(1), torch.full_like(table, -1))
+    api.check()
+    assert p.status.tolist() == [1, 0] and p.slots.tolist() == [-1] * 40
