@@ -18,9 +18,26 @@ from . import _lib as L
 _DTYPES = {torch.float32: L.TQ_F32, torch.bfloat16: L.TQ_BF16, torch.float16: L.TQ_F16}
 
 
+# the handle of a device's current stream, without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream=None) -> int:
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """What a call on `stream` (None: the current one) returns.  The memory
+    belongs to that stream: none that another one still works on, and none
+    that another one gets while the call runs."""
+    if stream is None or stream.cuda_stream == _raw_stream(torch.cuda.current_device() if device.index is None
+                                                           else device.index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                           else torch.cuda.ExternalStream(stream.cuda_stream, device)):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -157,12 +174,16 @@ class PackedCache:
                    if t is not None)
 
 
-def empty_cache(qz: Quantizer, B: int, H: int, N: int, device="cuda") -> PackedCache:
+def empty_cache(qz: Quantizer, B: int, H: int, N: int, device="cuda", stream=None) -> PackedCache:
+    """An uninitialised cache of B x H x N records, for use on `stream`."""
     dev = torch.device(device)
-    codes = torch.empty((B, H, N, qz.code_bytes), dtype=torch.uint8, device=dev) if qz.bm > 0 else None
-    qjl = torch.empty((B, H, N, qz.qjl_bytes), dtype=torch.uint8, device=dev) if qz.prod else None
-    rn = torch.empty((B, H, N), dtype=torch.float32, device=dev) if qz.prod else None
-    return PackedCache(codes, torch.empty((B, H, N), dtype=torch.float32, device=dev), qjl, rn)
+
+    def empty(*last, dtype):
+        return _empty((B, H, N, *last), dtype, dev, stream)
+    codes = empty(qz.code_bytes, dtype=torch.uint8) if qz.bm > 0 else None
+    qjl = empty(qz.qjl_bytes, dtype=torch.uint8) if qz.prod else None
+    rn = empty(dtype=torch.float32) if qz.prod else None
+    return PackedCache(codes, empty(dtype=torch.float32), qjl, rn)
 
 
 def _as_bhn(x: torch.Tensor) -> torch.Tensor:
@@ -183,7 +204,7 @@ def encode(qz: Quantizer, x: torch.Tensor, out: Optional[PackedCache] = None, st
     # a channel-group quantizer reads its channels of a wider row
     assert (d == qz.d if qz.channels is None else d >= qz.d) and x4.stride(3) == 1 and x4.dtype in _DTYPES
     if out is None:
-        out = empty_cache(qz, B, H, N, x.device)
+        out = empty_cache(qz, B, H, N, x.device, stream)
     v = out.view()
     L.check(L.lib().tq_encode(ctypes.byref(qz.c_struct()), x4.data_ptr(), _DTYPES[x4.dtype], B, H, N,
                               x4.stride(0), x4.stride(1), x4.stride(2), ctypes.byref(v), _stream(stream)))
@@ -193,7 +214,7 @@ def encode(qz: Quantizer, x: torch.Tensor, out: Optional[PackedCache] = None, st
 def dequant(qz: Quantizer, cache: PackedCache, stream=None) -> torch.Tensor:
     """tq_dequant into a new fp32 tensor [B, H, N, d]."""
     B, H, N = cache.shape
-    out = torch.empty((B, H, N, qz.d), dtype=torch.float32, device=cache.norms.device)
+    out = _empty((B, H, N, qz.d), torch.float32, cache.norms.device, stream)
     v = cache.view()
     L.check(L.lib().tq_dequant(ctypes.byref(qz.c_struct()), ctypes.byref(v), B, H, N, out.data_ptr(),
                                _stream(stream)))
@@ -345,8 +366,8 @@ class Search:
         n_q, d = queries.shape
         assert n_q == self.n_q and d == self.qz.d and queries.is_contiguous() and queries.dtype in _DTYPES
         dev = queries.device
-        top_v = torch.empty((n_q, k), dtype=torch.float32, device=dev)
-        top_i = torch.empty((n_q, k), dtype=torch.int64, device=dev)
+        top_v = _empty((n_q, k), torch.float32, dev, stream)
+        top_i = _empty((n_q, k), torch.int64, dev, stream)
         v = db.view()
         L.check(L.lib().tq_search_topk(ctypes.byref(self.qz.c_struct()), ctypes.byref(v), self.n_db,
                                        queries.data_ptr(), _DTYPES[queries.dtype], n_q, k, top_v.data_ptr(),
@@ -362,11 +383,6 @@ def search_topk(qz: Quantizer, queries: torch.Tensor, db: PackedCache, k: int):
 
 
 # ------------------------------------------------------------ paged cache
-
-# the handle of a device's current stream, without a Stream object around it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda device: torch.cuda.current_stream(device).cuda_stream)
-
 
 def _call(device: int, stream, fn, *args) -> None:
     """fn(*args, stream) with `device` current, on `stream` or that device's
@@ -527,7 +543,7 @@ def paged_append(kq: Quantizer, vq: Quantizer, k: torch.Tensor, v: torch.Tensor,
         Hq = q.shape[1]
         assert q.shape == (T, Hq, d) and q.dtype is dt and q.get_device() == dev
         if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+            q_out = _empty((T, Hq, d), dt, q.device, stream)
         assert q_out.shape == q.shape
         _check(dev, dt, q_out=q_out)
     _call(dev, stream, L.lib().tq_paged_append, kq.c_ref(), vq.c_ref(), rp, pp, pos_stride, _DTYPES[dt], T, Hq, Hkv,
@@ -545,7 +561,7 @@ def paged_dequant(qz: Quantizer, cache: PackedCache, slots: torch.Tensor, dtype=
     _check(dev, torch.int64, slots=slots)
     _check_cache(dev, qz, cache, shape)
     if out is None:
-        out = torch.empty((T, H, qz.d), dtype=dtype, device=cache.norms.device)
+        out = _empty((T, H, qz.d), dtype, cache.norms.device, stream)
     assert out.shape == (T, H, qz.d) and out.dtype in _DTYPES
     _check(dev, out.dtype, out=out)
     _call(dev, stream, L.lib().tq_paged_dequant, qz.c_ref(), cache.c_ref(), n_pages, P, T, H, slots.data_ptr(),
@@ -556,7 +572,8 @@ def paged_dequant(qz: Quantizer, cache: PackedCache, slots: torch.Tensor, dtype=
 class PagedAttention:
     """Reusable tq_paged_attention call for batches of at most max_requests
     requests and max_tokens query rows (its workspace allocated once).  Calls
-    that may overlap on the GPU need an object each."""
+    that may overlap on the GPU need an object each, which is kept until they
+    have run."""
 
     def __init__(self, kq: Quantizer, vq: Quantizer, Hq: int, Hkv: int, max_requests: int, max_tokens: int,
                  device="cuda"):
@@ -593,7 +610,7 @@ class PagedAttention:
         if scale is None:
             scale = 1.0 / math.sqrt(d)
         if out is None:
-            out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+            out = _empty((T, Hq, d), dt, q.device, stream)
         else:
             assert out.shape == q.shape
             _check(dev, dt, out=out)

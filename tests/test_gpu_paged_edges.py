@@ -237,3 +237,42 @@ def test_a_plan_over_a_missing_page_is_reported():
     p = api.PagePlanner(2, 16, 40, device=DEV)(i32(14, 5), i32(40, 0), i32(8), i32(1), torch.full_like(table, -1))
     api.check()
     assert p.status.tolist() == [1, 0] and p.slots.tolist() == [-1] * 40
+
+
+@pytest.mark.parametrize("call", ["append", "dequant", "attend", "encode", "dequant all", "search"])
+def test_outputs_belong_to_the_stream_of_their_call(call):
+    """The memory of what a call on another stream returns: none that the
+    current stream has just let go of, and none that it gets next."""
+    kq, vq, q, kc, vc, table, kv_lens, cu = paged_problem(40, [64, 64], [300, 90], 8, 2, 128, 16, torch.bfloat16)
+    rope = api.Rope(torch.ones(64, device=DEV))
+    op = api.PagedAttention(kq, vq, 8, 2, 2, 128, device=DEV)
+    slots = torch.arange(128, device=DEV)
+    places, queries = slots.int(), q[:, 0].contiguous()
+    find = api.Search(kq, 128, 2048, device=DEV)
+    db = api.encode(kq, torch.randn((2048, 128), generator=gen(1), device=DEV))
+    rows = q.permute(1, 0, 2)[None].contiguous()
+    run = {
+        "append": lambda s: api.paged_append(kq, vq, q[:, :2], q[:, :2], *caches, slots, q=q, rope=rope,
+                                             positions=places, stream=s),
+        "dequant": lambda s: api.paged_dequant(kq, kc, slots, stream=s),
+        "attend": lambda s: op(q, kc, vc, table, kv_lens, cu_q=cu, max_q=64, stream=s),
+        "encode": lambda s: api.encode(kq, rows, stream=s).codes,
+        "dequant all": lambda s: api.dequant(kq, kc, stream=s),
+        "search": lambda s: find(queries, db, 10, stream=s)[1],
+    }[call]
+    caches = [api.empty_cache(z, 8, 2, 16, device=DEV) for z in (kq, vq)]
+    side = torch.cuda.Stream()
+    for s in (side, torch.cuda.ExternalStream(side.cuda_stream)):
+        want = run(None)
+        torch.cuda.synchronize()
+        gone = torch.empty_like(want)
+        before = gone.data_ptr()
+        del gone
+        got = run(s)
+        at = got.data_ptr()
+        s.synchronize()
+        assert torch.equal(got, want) and at != before
+        torch.cuda.synchronize()
+        del got
+        assert torch.empty_like(want).data_ptr() != at
+    assert torch.equal(run(torch.cuda.current_stream()), want)
