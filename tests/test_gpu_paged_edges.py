@@ -276,3 +276,37 @@ def test_outputs_belong_to_the_stream_of_their_call(call):
         del got
         assert torch.empty_like(want).data_ptr() != at
     assert torch.equal(run(torch.cuda.current_stream()), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_rows_named_too_often_are_refused(dtype):
+    """Forty requests of the same 300 rows make more tiles than the call's 300
+    rows have, which the workspace has no room for: none is worked on."""
+    kq, vq, q, kc, vc, table, kv_lens, cu = paged_problem(41, [300], [350], 4, 2, 128, 16, dtype)
+    many = torch.tensor([0, 300] * 40 + [0], dtype=torch.int32, device=DEV)
+    op = api.PagedAttention(kq, vq, 4, 2, 80, 300, device=DEV)
+    out, lse = torch.full_like(q, 5.0), torch.full((300, 4), 7.0, device=DEV)
+    op(q, kc, vc, table.repeat(80, 1), kv_lens.repeat(80), cu_q=many, max_q=300, out=out, lse=lse)
+    refused()
+    assert bool((out == 5.0).all()) and bool((lse == 7.0).all())
+    check_attention((kq, vq, q, kc, vc, table, kv_lens, cu), op=op)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("qs", [[3, 1], [70, 1]])
+def test_large_scales(qs, dtype):
+    """Logits of a few tens and more: one or two tokens carry a row."""
+    for scale in (5.0 / math.sqrt(128), -20.0 / math.sqrt(128)):
+        kq, vq, q, kc, vc, table, kv_lens, cu = p = paged_problem(9, qs, [90, 70], 4, 2, 128, 16, dtype)
+        want, want_lse, tol, lse_tol = attention_ref(*p, scale, True, 0)
+        lse = torch.empty(q.shape[:2], device=DEV)
+        out = api.PagedAttention(kq, vq, 4, 2, 2, sum(qs), device=DEV)(
+            q, kc, vc, table, kv_lens, cu_q=cu, max_q=max(qs), scale=scale, lse=lse)
+        api.check()
+        off = np.abs(host(out).astype(np.float64) - want)
+        assert np.all(np.abs(host(lse) - want_lse) <= lse_tol)
+        # a logit off by delta moves its weight by a factor exp(delta): to first order what tol holds, and beyond it
+        # by exp(2 delta) - 1 over 2 delta at most
+        grow = np.expm1(2 * lse_tol) / (2 * lse_tol)
+        assert np.all(off <= tol * grow[..., None] + torch.finfo(dtype).eps / 2 * np.abs(want) * 1.01
+                      + torch.finfo(dtype).tiny)
