@@ -420,7 +420,8 @@ tq_status tq_paged_dequant(const tq_quantizer *q, const tq_cache_view *cache, in
  * optional [T][Hq] fp32, the natural logarithm of the softmax's sum.  A row
  * that sees no token, or only logits of -inf, gets zeros (lse -inf); rows
  * behind cu_q[R] are left as they were.  max_q: an upper bound of the requests'
- * row counts; it sizes the work and never changes which rows are computed.
+ * row counts; it chooses the kernel (one far above them makes a decode batch
+ * slow) and never changes which rows are computed.
  * d is 64, 128 or 256, page_size a multiple of 16, R < 2^24.
  * workspace: DEVICE, at least tq_paged_attention_workspace_bytes(...) bytes,
  * 16-byte aligned, else TQ_EWORKSPACE; calls that may overlap on the GPU need

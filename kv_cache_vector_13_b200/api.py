@@ -592,9 +592,11 @@ class PagedAttention:
         """Attention of the query rows q [T, Hq, d] (bf16 or fp16): request r
         owns rows cu_q[r]:cu_q[r+1] (cu_q None: one row each), its cached
         tokens are the kv_lens[r] ones of the pages block_table[r] (its own
-        rows' included).  max_q: an upper bound of the row counts (default:
-        1 without cu_q, else T).  Returns out [T, Hq, d] in q's dtype; lse
-        [T, Hq] (fp32), if given, gets the logarithm of the softmax's sums."""
+        rows' included).  max_q: an upper bound of the row counts, by which the
+        kernel is chosen (default: 1 without cu_q, else T, which for a batch of
+        many requests takes tiles of 128 or 256 rows for a few: give it).
+        Returns out [T, Hq, d] in q's dtype; lse [T, Hq] (fp32), if given, gets
+        the logarithm of the softmax's sums."""
         (T, Hq, d), (R,), dt, dev = q.shape, kv_lens.shape, q.dtype, self.device
         n_pages, Hkv, P = shape = kcache.norms.shape
         assert (Hq, Hkv, d) == (self.Hq, self.Hkv, self.kq.d) and vcache.norms.shape == shape

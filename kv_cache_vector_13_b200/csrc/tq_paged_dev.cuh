@@ -50,8 +50,9 @@ __device__ __forceinline__ float value_log2(float norm) {
 // [1, 2) moves them to where fp16 holds them best.  What counts is the error
 // of a Gaussian coordinate's square, weighted by how often each level comes
 // up, apart from a gain common to all levels, which the kernels divide out:
-// over 192 candidates, one a thread, it falls from 2e-4 to 8e-5 of a
-// coordinate (d = 128; 4e-5 with 1024, for 5 us more a call).
+// over 192 candidates, one for every two threads of the block (256 on the large
+// tiles, 128 for d = 256), it falls from 2e-4 to 8e-5 of a coordinate (d = 128;
+// 4e-5 with 1024, for 5 us more a call).
 
 // P(|N(0,1)| in the level's cell) times the level squared, over their sum, for
 // the positive levels of the 16-level Lloyd-Max quantizer.

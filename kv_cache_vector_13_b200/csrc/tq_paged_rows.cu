@@ -42,9 +42,9 @@
 // of a KV head (128 of them the byte permutes and table reads) at half of the
 // issue slots, and by what a piece costs besides its steps, about 5 us.
 // Measured on a B200: d = 128, 32 / 8 heads, bf16, 4 requests of up to 262144
-// tokens (731 MB) 188 us, 3.9 TB/s; 16 of up to 65536 (551 MB) 147 us, 3.7
-// TB/s; 1 x 32768 tokens 23 us, of which 11.5 are left with a single step; 128
-// requests of 4 rows and up to 4001 tokens, 64 / 8 heads, fp16, 327 us; d =
+// tokens (731 MB) 188 us, 3.9 TB/s; 16 of up to 65536 (551 MB) 148 us, 3.7
+// TB/s; 1 x 32768 tokens 23.5 us, of which 11.5 are left with a single step; 128
+// requests of 4 rows and up to 4001 tokens, 64 / 8 heads, fp16, 330 us; d =
 // 256, 16 requests of up to 4001 tokens, 32 / 8 heads, bf16, 40 us.
 
 #include "../../include/tq.h"

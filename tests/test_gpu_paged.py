@@ -19,8 +19,8 @@ the rotated basis, the error rotated back), weights below fp16's normal range
 output's half step.  lse moves by at most the largest delta_j.  Over a whole
 output the errors average: its relative 2-norm error stays within the
 framework's 2e-3 (and the output's rounding).  Up to 8 query rows a KV head
-are carried as hi + lo pairs: there every row holds the framework's decode
-bar, 2e-3 of its largest output."""
+every row holds the framework's decode bar, 2e-3 of its largest output (up to
+4, and for fp16 outputs, rows and weights are carried as hi + lo pairs)."""
 
 import math
 
@@ -494,7 +494,7 @@ def test_scale_sign_and_large_logits():
 
 
 def test_query_rows_of_any_size():
-    # rows of 1e4 and 1e-6: the fp16 operands are scaled by the row
+    # rows of 1e4 and 1e-4: the fp16 operands are scaled by the row
     for f in (1e4, 1e-4):
         kq, vq, q, kc, vc, table, kv_lens, cu = paged_problem(10, [3, 1, 40], [90, 70, 60], 4, 2, 128, 16, torch.bfloat16)
         check_attention((kq, vq, (q.float() * f).to(torch.bfloat16), kc, vc, table, kv_lens, cu), scale=0.088 / f)
